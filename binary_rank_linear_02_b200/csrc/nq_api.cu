@@ -16,6 +16,8 @@ constexpr int64_t kMaxDim = int64_t(1) << 20;
 constexpr int64_t kMaxRank = 65536;
 constexpr int64_t kMaxElems = int64_t(1) << 40;  // element-wise helpers: elements per call
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;  // one CTA per row
+constexpr int64_t kMaxListed = 1024;                  // teacher entries per token
+constexpr int64_t kMaxXentTokens = int64_t(1) << 24;
 // From this many tokens the factor gradients take the prefill GEMM for t and u and the
 // tensor cores for the sums over the tokens; below, the decode stage 1 and a SIMT kernel.
 constexpr int64_t kFactorTcMinBatch = 64;
@@ -827,6 +829,9 @@ int nq_device_status(void* stream) {
     unsigned word = 0;
     if (cudaMemcpy(&word, ws->status + 1, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess) return NQ_ERR_CUDA;
     if (word != 0 && cudaMemset(ws->status + 1, 0, sizeof(unsigned)) != cudaSuccess) return NQ_ERR_CUDA;
+    unsigned head = 0;  // the cross entropy's kernels have a word of their own
+    if (xent_take_status(&head) != NQ_OK) return NQ_ERR_CUDA;
+    if (word == 0 && head != 0) return -(int)head;
     // a kernel that gave up may have left arrival counters part-way: start them from zero again
     if (word != 0 && cudaMemset(ws->counters, 0, sizeof(int) * (ws->counter_cap + 1)) != cudaSuccess)
         return NQ_ERR_CUDA;
@@ -929,6 +934,148 @@ int nq_lowrank_linear_fwd(const void* x, const uint32_t* Upk, const uint32_t* Vp
     d.n = n;
     d.r = r;
     return grouped_run(&d, sizeof(d), nullptr, 1, batch, stream);
+}
+
+// ---------------------------------------------------------------- the output head
+
+// The head's entry points take device pointers alone, 16-byte aligned; null ones are optional.
+static int check_device_pointers(const void* const* ptrs, int count) {
+    for (int i = 0; i < count; ++i)
+        if (ptrs[i] && !aligned16(ptrs[i])) return NQ_ERR_ALIGN;
+    for (int i = 0; i < count; ++i)
+        if (ptrs[i] && pointer_kind(ptrs[i]) != kDeviceMem) return NQ_ERR_PTRKIND;
+    return NQ_OK;
+}
+
+int nq_pack_q4(const uint8_t* codes, int64_t rows, int64_t cols, uint32_t* out, void* stream) {
+    if (rows < 0 || cols < 0) return NQ_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return NQ_OK;
+    if (!codes || !out) return NQ_ERR_NULL;
+    if (rows > (int64_t(1) << 40) / cols) return NQ_ERR_SHAPE;
+    const int kc = pointer_kind(codes), ko = pointer_kind(out);
+    if (kc != ko || kc == kForeignMem) return NQ_ERR_PTRKIND;
+    const int64_t wpr = (cols + 7) / 8;
+    if (kc == kHostMem) {
+        for (int64_t i = 0; i < rows * cols; ++i)
+            if (codes[i] > 15) return NQ_ERR_VALUE;
+        for (int64_t row = 0; row < rows; ++row) {
+            for (int64_t w = 0; w < wpr; ++w) {
+                uint32_t word = 0;
+                for (int64_t b = 0; b < 8 && 8 * w + b < cols; ++b)
+                    word |= (uint32_t)codes[row * cols + 8 * w + b] << (4 * b);
+                out[row * wpr + w] = word;
+            }
+        }
+        return NQ_OK;
+    }
+    int st = NQ_OK;
+    Workspace* ws = workspace_for(128, 128, 128, 0, DecodeNeed(), &st);
+    if (!ws) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(ws->status, 0, sizeof(unsigned), s) != cudaSuccess) return NQ_ERR_CUDA;
+    st = q4_pack_device(codes, rows, cols, out, ws->status, s);
+    if (st != NQ_OK) return st;
+    unsigned flag = 0;
+    if (cudaMemcpyAsync(&flag, ws->status, sizeof(unsigned), cudaMemcpyDeviceToHost, s) != cudaSuccess)
+        return NQ_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return NQ_ERR_CUDA;
+    return flag ? NQ_ERR_VALUE : NQ_OK;
+}
+
+int nq_q4_linear_fwd(const void* x, const uint32_t* Wq, const void* scales, const void* zeros, int64_t m, int64_t n,
+                     int64_t group, int64_t batch, float* y, void* stream) {
+    if (batch < 0 || batch > kQ4MaxBatch) return NQ_ERR_BATCH;
+    if (m <= 0 || n <= 0 || n % 128 || m > kMaxDim || n > kMaxDim) return NQ_ERR_SHAPE;
+    if (group != 32 && group != 64 && group != 128) return NQ_ERR_SHAPE;
+    if (batch == 0) return NQ_OK;
+    if (!x || !Wq || !scales || !y) return NQ_ERR_NULL;
+    const void* ptrs[] = {x, Wq, scales, zeros, y};
+    const int st = check_device_pointers(ptrs, 5);
+    if (st != NQ_OK) return st;
+    return q4_forward(static_cast<const uint16_t*>(x), Wq, static_cast<const uint16_t*>(scales),
+                      static_cast<const uint16_t*>(zeros), m, n, (int)group, batch, y,
+                      static_cast<cudaStream_t>(stream));
+}
+
+static int check_distill(int logits_type, int64_t ld, int64_t tokens, int64_t vocab, int64_t k, float temperature) {
+    if (tokens < 0 || tokens > kMaxRows) return NQ_ERR_BATCH;
+    if (vocab <= 0 || vocab > kMaxDim || ld < vocab || ld > 2 * kMaxDim || k <= 0 || k > kMaxListed) return NQ_ERR_SHAPE;
+    if (logits_type != NQ_F32 && logits_type != NQ_BF16) return NQ_ERR_VALUE;
+    if (!(temperature > 0.f) || temperature > 3.4e38f) return NQ_ERR_VALUE;
+    return NQ_OK;
+}
+
+int nq_distill_topk_fwd(const void* logits, int logits_type, int64_t ld, const int32_t* ids, const float* teacher,
+                        const float* teacher_lse, int64_t tokens, int64_t vocab, int64_t k, float temperature,
+                        float* loss, void* stream) {
+    int st = check_distill(logits_type, ld, tokens, vocab, k, temperature);
+    if (st != NQ_OK) return st;
+    if (tokens == 0) return NQ_OK;
+    if (!logits || !ids || !teacher || !loss) return NQ_ERR_NULL;
+    const void* ptrs[] = {logits, ids, teacher, teacher_lse, loss};
+    if ((st = check_device_pointers(ptrs, 5)) != NQ_OK) return st;
+    return distill_device(logits, logits_type == NQ_BF16, ld, ids, teacher, teacher_lse, nullptr, tokens, vocab, k,
+                          temperature, loss, nullptr, false, static_cast<cudaStream_t>(stream));
+}
+
+int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const int32_t* ids, const float* teacher,
+                        const float* teacher_lse, const float* dloss, int64_t tokens, int64_t vocab, int64_t k,
+                        float temperature, float* loss, void* dlogits, int grad_type, void* stream) {
+    int st = check_distill(logits_type, ld, tokens, vocab, k, temperature);
+    if (st != NQ_OK) return st;
+    if (grad_type != NQ_F32 && grad_type != NQ_BF16) return NQ_ERR_VALUE;
+    if (tokens == 0) return NQ_OK;
+    if (!logits || !ids || !teacher || !dloss || !dlogits) return NQ_ERR_NULL;
+    const void* ptrs[] = {logits, ids, teacher, teacher_lse, dloss, loss, dlogits};
+    if ((st = check_device_pointers(ptrs, 7)) != NQ_OK) return st;
+    return distill_device(logits, logits_type == NQ_BF16, ld, ids, teacher, teacher_lse, dloss, tokens, vocab, k,
+                          temperature, loss, dlogits, grad_type == NQ_BF16, static_cast<cudaStream_t>(stream));
+}
+
+static int check_xent(int64_t tokens, int64_t vocab, int64_t d) {
+    if (tokens < 0 || tokens > kMaxXentTokens) return NQ_ERR_BATCH;
+    if (vocab <= 0 || vocab > kMaxDim || d <= 0 || d % 8 || d > kMaxDim) return NQ_ERR_SHAPE;
+    return NQ_OK;
+}
+
+int64_t nq_linear_cross_entropy_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d, int backward) {
+    if (check_xent(tokens, vocab, d) != NQ_OK) return -1;
+    if (tokens == 0) return 0;
+    return backward ? xent_bwd_scratch_bytes(tokens, vocab, d) : xent_fwd_scratch_bytes(tokens, vocab);
+}
+
+int nq_linear_cross_entropy_fwd(const void* h, const void* W, const int32_t* labels, int64_t tokens, int64_t vocab,
+                                int64_t d, float* loss, float* lse, void* scratch, int64_t scratch_bytes, void* stream) {
+    int st = check_xent(tokens, vocab, d);
+    if (st != NQ_OK) return st;
+    if (tokens == 0) return NQ_OK;
+    if (!h || !W || !labels || !loss || !lse || !scratch) return NQ_ERR_NULL;
+    const void* ptrs[] = {h, W, labels, loss, lse, scratch};
+    if ((st = check_device_pointers(ptrs, 6)) != NQ_OK) return st;
+    if (scratch_bytes < xent_fwd_scratch_bytes(tokens, vocab)) return NQ_ERR_NOMEM;
+    return xent_forward(static_cast<const uint16_t*>(h), static_cast<const uint16_t*>(W), labels, tokens, vocab, d, loss,
+                        lse, scratch, static_cast<cudaStream_t>(stream));
+}
+
+int nq_linear_cross_entropy_bwd(const void* h, const void* W, const int32_t* labels, const float* lse,
+                                const float* dloss, int64_t tokens, int64_t vocab, int64_t d, void* dh, void* dW,
+                                void* scratch, int64_t scratch_bytes, void* stream) {
+    int st = check_xent(tokens, vocab, d);
+    if (st != NQ_OK) return st;
+    if (!dh && !dW) return NQ_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tokens == 0) {  // empty sums
+        if (!dW) return NQ_OK;
+        const void* out[] = {dW};
+        if ((st = check_device_pointers(out, 1)) != NQ_OK) return st;
+        return cudaMemsetAsync(dW, 0, sizeof(uint16_t) * (size_t)vocab * (size_t)d, s) == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+    }
+    if (!h || !W || !labels || !lse || !dloss || !scratch) return NQ_ERR_NULL;
+    const void* ptrs[] = {h, W, labels, lse, dloss, dh, dW, scratch};
+    if ((st = check_device_pointers(ptrs, 8)) != NQ_OK) return st;
+    if (scratch_bytes < xent_bwd_scratch_bytes(tokens, vocab, d)) return NQ_ERR_NOMEM;
+    return xent_backward(static_cast<const uint16_t*>(h), static_cast<const uint16_t*>(W), labels, lse, dloss, tokens,
+                         vocab, d, static_cast<uint16_t*>(dh), static_cast<uint16_t*>(dW), scratch, s);
 }
 
 }  // extern "C"

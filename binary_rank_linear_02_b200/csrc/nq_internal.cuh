@@ -159,4 +159,25 @@ int cast_f32_bf16_device(const float* src, int64_t count, uint16_t* dst, cudaStr
 int envelope_sum_device(float* y, const float* terms, int nterms, int64_t count, cudaStream_t stream);
 int rms_normalize_bf16_device(const float* src, int64_t rows, int64_t cols, uint16_t* dst, cudaStream_t stream);
 
+// ---------------------------------------------------------------- the output head
+// Largest decode grid of q4_forward: 65535 groups of 8 tokens.
+constexpr int64_t kQ4MaxBatch = 65535 * int64_t(8);
+int q4_forward(const uint16_t* x, const uint32_t* W, const uint16_t* scales, const uint16_t* zeros, int64_t m,
+               int64_t n, int group, int64_t batch, float* y, cudaStream_t stream);
+int q4_pack_device(const uint8_t* codes, int64_t rows, int64_t cols, uint32_t* out, unsigned* flag,
+                   cudaStream_t stream);
+// dlogits null: the loss alone (then dloss is not read); loss may be null with dlogits
+int distill_device(const void* logits, bool logits_bf16, int64_t ld, const int32_t* ids, const float* teacher,
+                   const float* teacher_lse, const float* dloss, int64_t tokens, int64_t vocab, int64_t k,
+                   float temperature, float* loss, void* dlogits, bool grad_bf16, cudaStream_t stream);
+int64_t xent_fwd_scratch_bytes(int64_t tokens, int64_t vocab);
+int64_t xent_bwd_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d);
+int xent_forward(const uint16_t* h, const uint16_t* W, const int32_t* labels, int64_t tokens, int64_t vocab, int64_t d,
+                 float* loss, float* lse, void* scratch, cudaStream_t stream);
+int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, const float* lse, const float* dloss,
+                  int64_t tokens, int64_t vocab, int64_t d, uint16_t* dh, uint16_t* dW, void* scratch,
+                  cudaStream_t stream);
+// reads and clears the status word of the cross entropy's kernels (the device is idle)
+int xent_take_status(unsigned* word);
+
 }  // namespace nq

@@ -34,6 +34,8 @@ NQ_ERR_PTRKIND = -9
 NQ_ERR_NOALLOC_LIMIT = -10
 NQ_DECODE_MAX_BATCH = 8
 NQ_NOALLOC_MAX_RANK = 4096
+NQ_F32 = 0
+NQ_BF16 = 1
 
 
 class nq_linear_desc(ctypes.Structure):
@@ -105,6 +107,21 @@ def _load() -> ctypes.CDLL:
     L.nq_admm_iterate.restype = ctypes.c_int
     L.nq_admm_factorize.argtypes = [p, i64, i64, i64, p, i32, i32, f64, f64, p, p, p, p, p, p]
     L.nq_admm_factorize.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    L.nq_pack_q4.argtypes = [p, i64, i64, p, p]
+    L.nq_pack_q4.restype = i32
+    L.nq_q4_linear_fwd.argtypes = [p, p, p, p, i64, i64, i64, i64, p, p]
+    L.nq_q4_linear_fwd.restype = i32
+    L.nq_distill_topk_fwd.argtypes = [p, i32, i64, p, p, p, i64, i64, i64, f32, p, p]
+    L.nq_distill_topk_fwd.restype = i32
+    L.nq_distill_topk_bwd.argtypes = [p, i32, i64, p, p, p, p, i64, i64, i64, f32, p, p, i32, p]
+    L.nq_distill_topk_bwd.restype = i32
+    L.nq_linear_cross_entropy_scratch_bytes.argtypes = [i64, i64, i64, i32]
+    L.nq_linear_cross_entropy_scratch_bytes.restype = i64
+    L.nq_linear_cross_entropy_fwd.argtypes = [p, p, p, i64, i64, i64, p, p, p, i64, p]
+    L.nq_linear_cross_entropy_fwd.restype = i32
+    L.nq_linear_cross_entropy_bwd.argtypes = [p, p, p, p, p, i64, i64, i64, p, p, p, i64, p]
+    L.nq_linear_cross_entropy_bwd.restype = i32
     return L
 
 
@@ -474,3 +491,176 @@ def lowrank_linear_fwd_envelope(x, Upk, Vpk, a, b, m: int, n: int, r: int, y=Non
 def bits_per_weight_envelope(m: int, n: int, r: int, l: int) -> float:
     return _lib.nq_bits_per_weight_envelope(m, n, r, l)
 
+
+# ------------------------------------------------------------------ the output head
+
+def _typed(t, name: str, *dtypes) -> None:
+    """The head's calls pass pointers of typed buffers on: a wrong element type is refused here."""
+    if t is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, want {' or '.join(str(d) for d in dtypes)}")
+
+
+def _shaped(t, name: str, *shape) -> None:
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, want {shape}")
+
+
+def pack_q4(codes, out=None, stream=None):
+    """rows x cols uint8 codes 0 .. 15 (torch tensor or numpy array) -> rows x ceil(cols/8) words."""
+    rows, cols = codes.shape
+    wpr = (cols + 7) // 8
+    if isinstance(codes, np.ndarray):
+        if codes.dtype != np.uint8:
+            raise TypeError(f"codes: {codes.dtype}, want uint8")
+        if out is None:
+            out = np.empty((rows, wpr), dtype=np.uint32)
+    else:
+        import torch
+
+        _typed(codes, "codes", torch.uint8)
+        if out is None:
+            out = torch.empty((rows, wpr), dtype=torch.int32, device=codes.device)
+    _check(_lib.nq_pack_q4(_ptr(codes), rows, cols, _ptr(out), _stream(stream, codes)), "nq_pack_q4")
+    return out
+
+
+def q4_linear_fwd(x, Wq, scales, m: int, n: int, group: int, zeros=None, y=None, stream=None):
+    """y (batch x m, float32) = x W^T, W[i][j] = scales[i][j // group] (code[i][j] - zeros[i][j // group]).
+
+    x: batch x n (or n) bfloat16; Wq: m x n/8 words of pack_q4; scales and zeros: m x n/group
+    fp16 (zeros None: 8 everywhere); bfloat16 and fp16 may be given as int16 bit patterns.
+    """
+    import torch
+
+    batch = x.shape[0] if x.dim() == 2 else 1
+    _typed(x, "x", torch.bfloat16, torch.int16)
+    _typed(Wq, "Wq", torch.int32, torch.uint32)
+    _typed(scales, "scales", torch.float16, torch.int16)
+    _typed(zeros, "zeros", torch.float16, torch.int16)
+    _shaped(x, "x", *((batch, n) if x.dim() == 2 else (n,)))
+    _shaped(Wq, "Wq", m, n // 8)
+    if group in (32, 64, 128):  # any other group is the library's to refuse
+        _shaped(scales, "scales", m, n // group)
+        _shaped(zeros, "zeros", m, n // group)
+    if y is None:
+        y = torch.empty((batch, m), dtype=torch.float32, device=x.device)
+    _typed(y, "y", torch.float32)
+    _check(_lib.nq_q4_linear_fwd(_ptr(x), _ptr(Wq), _ptr(scales), _ptr(zeros), m, n, group, batch, _ptr(y),
+                                 _stream(stream, x)), "nq_q4_linear_fwd")
+    return y
+
+
+def _logit_type(dtype) -> int:
+    import torch
+
+    if dtype == torch.float32:
+        return NQ_F32
+    if dtype == torch.bfloat16:
+        return NQ_BF16
+    raise TypeError(f"logits: {dtype}, want torch.float32 or torch.bfloat16")
+
+
+def _distill_args(logits, ids, teacher, vocab, teacher_lse, dloss=None):
+    import torch
+
+    tokens, ld = logits.shape
+    k = ids.shape[1]
+    _typed(ids, "ids", torch.int32)
+    for t, name in ((teacher, "teacher"), (teacher_lse, "teacher_lse"), (dloss, "dloss")):
+        _typed(t, name, torch.float32)
+    _shaped(ids, "ids", tokens, k)
+    _shaped(teacher, "teacher", tokens, k)
+    _shaped(teacher_lse, "teacher_lse", tokens)
+    _shaped(dloss, "dloss", tokens)
+    return tokens, ld, k, _logit_type(logits.dtype)
+
+
+def distill_topk_fwd(logits, ids, teacher, vocab: int, temperature: float = 1.0, teacher_lse=None, loss=None,
+                     stream=None):
+    """loss (tokens, float32) of the student's logits (tokens x ld, float32 or bfloat16, the
+    first `vocab` columns) against the teacher's entries: ids (tokens x k int32, -1: absent) and
+    their logits `teacher` (tokens x k float32); teacher_lse (tokens float32): log sum exp of the
+    teacher's logits / temperature over its whole vocabulary, None: the teacher restricted to its list."""
+    import torch
+
+    tokens, ld, k, kind = _distill_args(logits, ids, teacher, vocab, teacher_lse)
+    if loss is None:
+        loss = torch.empty((tokens,), dtype=torch.float32, device=logits.device)
+    _check(_lib.nq_distill_topk_fwd(_ptr(logits), kind, ld, _ptr(ids), _ptr(teacher), _ptr(teacher_lse), tokens, vocab,
+                                    k, temperature, _ptr(loss), _stream(stream, logits)), "nq_distill_topk_fwd")
+    return loss
+
+
+def distill_topk_bwd(logits, ids, teacher, vocab: int, dloss, temperature: float = 1.0, teacher_lse=None, dtype=None,
+                     dlogits=None, loss=None, stream=None):
+    """(dlogits, loss): the gradient of sum_i dloss[i] loss[i] with respect to the logits
+    (tokens x ld, torch.bfloat16 unless `dtype` says torch.float32; columns from `vocab` on are
+    zero) and the losses, from one read of the logits.  Arguments as distill_topk_fwd."""
+    import torch
+
+    tokens, ld, k, kind = _distill_args(logits, ids, teacher, vocab, teacher_lse, dloss)
+    if dlogits is None:
+        dlogits = torch.empty((tokens, ld), dtype=dtype or torch.bfloat16, device=logits.device)
+    _shaped(dlogits, "dlogits", tokens, ld)
+    if loss is None:
+        loss = torch.empty((tokens,), dtype=torch.float32, device=logits.device)
+    _check(_lib.nq_distill_topk_bwd(_ptr(logits), kind, ld, _ptr(ids), _ptr(teacher), _ptr(teacher_lse), _ptr(dloss),
+                                    tokens, vocab, k, temperature, _ptr(loss), _ptr(dlogits),
+                                    _logit_type(dlogits.dtype), _stream(stream, logits)), "nq_distill_topk_bwd")
+    return dlogits, loss
+
+
+def _xent_args(h, W, labels):
+    import torch
+
+    tokens, d = h.shape
+    vocab = W.shape[0]
+    _typed(h, "h", torch.bfloat16, torch.int16)
+    _typed(W, "W", torch.bfloat16, torch.int16)
+    _typed(labels, "labels", torch.int32)
+    _shaped(W, "W", vocab, d)
+    _shaped(labels, "labels", tokens)
+    return tokens, vocab, d
+
+
+def _xent_scratch(tokens: int, vocab: int, d: int, backward: bool, device):
+    import torch
+
+    size = _lib.nq_linear_cross_entropy_scratch_bytes(tokens, vocab, d, int(backward))
+    # at least a byte, so that the pointer is one; sizes out of range are the call's to refuse
+    return torch.empty((max(size, 16),), dtype=torch.uint8, device=device), size
+
+
+def linear_cross_entropy_fwd(h, W, labels, loss=None, lse=None, stream=None):
+    """(loss, lse), float32 per token: cross entropy of softmax(h W^T) against int32 labels (a
+    label outside the vocabulary does not count: loss 0), without the logits in memory.
+    h: tokens x d, W: vocab x d, bfloat16."""
+    import torch
+
+    tokens, vocab, d = _xent_args(h, W, labels)
+    loss = torch.empty((tokens,), dtype=torch.float32, device=h.device) if loss is None else loss
+    lse = torch.empty((tokens,), dtype=torch.float32, device=h.device) if lse is None else lse
+    _typed(loss, "loss", torch.float32)
+    _typed(lse, "lse", torch.float32)
+    scratch, size = _xent_scratch(tokens, vocab, d, False, h.device)
+    _check(_lib.nq_linear_cross_entropy_fwd(_ptr(h), _ptr(W), _ptr(labels), tokens, vocab, d, _ptr(loss), _ptr(lse),
+                                            _ptr(scratch), size, _stream(stream, h)), "nq_linear_cross_entropy_fwd")
+    return loss, lse
+
+
+def linear_cross_entropy_bwd(h, W, labels, lse, dloss, need_dh: bool = True, need_dW: bool = True, stream=None):
+    """(dh (tokens x d), dW (vocab x d)) bfloat16, None for one that is not needed: the gradients
+    of sum_i dloss[i] loss[i], from the lse that linear_cross_entropy_fwd gave."""
+    import torch
+
+    tokens, vocab, d = _xent_args(h, W, labels)
+    for t, name in ((lse, "lse"), (dloss, "dloss")):
+        _typed(t, name, torch.float32)
+        _shaped(t, name, tokens)
+    dh = torch.empty((tokens, d), dtype=torch.bfloat16, device=h.device) if need_dh else None
+    dW = torch.empty((vocab, d), dtype=torch.bfloat16, device=h.device) if need_dW else None
+    scratch, size = _xent_scratch(tokens, vocab, d, True, h.device)
+    _check(_lib.nq_linear_cross_entropy_bwd(_ptr(h), _ptr(W), _ptr(labels), _ptr(lse), _ptr(dloss), tokens, vocab, d,
+                                            _ptr(dh), _ptr(dW), _ptr(scratch), size, _stream(stream, h)),
+           "nq_linear_cross_entropy_bwd")
+    return dh, dW

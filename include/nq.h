@@ -344,6 +344,116 @@ int nq_lowrank_linear_fwd_noalloc(const void* x, const uint32_t* Upk, const uint
                                   int64_t batch, float* y, void* stream);
 
 /*
+ * The output head.  A quantised decoder ends in a layer that is often not factorised and, in
+ * the refinement step, in a loss whose gradient is the dy of the backward calls above.  The
+ * pages print neither (hardwired.dev, "Krok 3", names the refinement alone); these entry
+ * points are the library's own.  They use no library workspace: what they need beyond their
+ * arguments is the caller's `scratch`, so that calls on different streams, and captured
+ * graphs, share nothing.  Every pointer is device memory of the current device (else
+ * NQ_ERR_PTRKIND), 16-byte aligned (else NQ_ERR_ALIGN); outputs overlap no other buffer of
+ * the call; the calls are asynchronous on `stream`.
+ */
+
+/* Element types of logits and their gradients. */
+#define NQ_F32 0
+#define NQ_BF16 1
+
+/*
+ * nq_pack_q4 -- store 4-bit codes eight to a word: code j of a row in bits 4 (j % 8) .. + 3 of
+ * word j / 8 (unused bits of a row's last word are 0).
+ *   codes : rows x cols uint8, row-major, each 0 .. 15
+ *   out   : rows x ceil(cols/8) uint32
+ * Pointer kinds, empty sizes, synchronisation and NQ_ERR_VALUE (a code above 15) as
+ * nq_pack_signs.
+ */
+int nq_pack_q4(const uint8_t* codes, int64_t rows, int64_t cols, uint32_t* out, void* stream);
+
+/*
+ * nq_q4_linear_fwd -- y = x W^T for a layer kept at 4 bits per weight with a scale per group:
+ *     W[i][j] = s[i][j / group] * (c[i][j] - z[i][j / group]).
+ *   x      : batch x n bfloat16
+ *   Wq     : m x (n/8) uint32, the codes c (nq_pack_q4)
+ *   scales : m x (n/group) fp16;  zeros : m x (n/group) fp16 (any value, in units of a code),
+ *            or NULL: every z is 8
+ *   y      : batch x m float32 (written)
+ *   group  : 32, 64 or 128 (else NQ_ERR_SHAPE);  n : a positive multiple of 128;  m >= 1 (any);
+ *            m, n at most 1<<20
+ *   batch  : 0 (a no-op) to 524280 (else NQ_ERR_BATCH).  Made for the few tokens of a decode
+ *            step: up to 8 tokens read the codes once, more read them again for every 8.
+ * Products are exact and sums are fp32: |error| <= (48 + n/256) 2^-23 sum_j |s| (|c - 8| +
+ * |z - 8|) |x_j|.  Each token's result does not depend on the others.
+ */
+int nq_q4_linear_fwd(const void* x, const uint32_t* Wq, const void* scales, const void* zeros, int64_t m, int64_t n,
+                     int64_t group, int64_t batch, float* y, void* stream);
+
+/*
+ * nq_distill_topk_fwd, nq_distill_topk_bwd -- the distillation loss of each token against the
+ * top logits its teacher kept, and its gradient.  With p = softmax(z / T) over the student's
+ * `vocab` logits z of a token, and the teacher's entries (id_k, u_k):
+ *     q_k  = exp(u_k / T) / sum_j exp(u_j / T), q_rest = 0              teacher_lse NULL: the
+ *            teacher restricted to its list;
+ *     q_k  = exp(u_k / T - teacher_lse), q_rest = max(0, 1 - sum_k q_k) teacher_lse given: the
+ *            logarithm of the sum of exp(u / T) over the teacher's whole vocabulary;
+ *     loss = T^2 (sum_k q_k log(q_k / p[id_k]) + q_rest log(q_rest / p_rest)),
+ *     dlogits[v] = dloss T (p_v (sum_k q_k + q_rest) - sum over k with id_k = v of q_k
+ *                           - [v not listed] q_rest p_v / p_rest),
+ * p_rest the sum of p over the classes that are not listed.  Terms with q = 0 are 0; the rest
+ * term is left out when no class outside the list has a finite logit.
+ *   logits  : tokens rows of `vocab` values of logits_type (NQ_F32 or NQ_BF16), rows `ld`
+ *             elements apart (ld >= vocab: a head padded to a multiple of 128)
+ *   ids     : tokens x k int32;  an id outside 0 .. vocab-1 (e.g. -1) is an absent entry, a
+ *             token without entries has loss 0 and gradient 0, whatever its logits are; the
+ *             masses of an id that is listed more than once add
+ *   teacher : tokens x k float32 (u);  teacher_lse : tokens float32 or NULL
+ *   dloss   : tokens float32, the loss's weight per token (bwd)
+ *   loss    : tokens float32 (written; may be NULL in bwd)
+ *   dlogits : rows as the logits' (same ld), of grad_type; columns vocab .. ld-1 are written
+ *             with 0, so that it can be the dy of a padded factorised head
+ *   vocab : 1 .. 1<<20;  ld : vocab .. 1<<21;  k : 1 .. 1024 (else NQ_ERR_SHAPE);
+ *   tokens : 0 (a no-op) .. 2^31-1 (else NQ_ERR_BATCH);  temperature > 0 and finite, types as
+ *   above (else NQ_ERR_VALUE).
+ * bwd reads the logits from memory once and gives loss and gradient of the same pass: it needs
+ * nothing from fwd.  Sums over the vocabulary are fp32, the loss's few logarithms and their
+ * differences fp64.  Repeated calls agree bit for bit.
+ */
+int nq_distill_topk_fwd(const void* logits, int logits_type, int64_t ld, const int32_t* ids, const float* teacher,
+                        const float* teacher_lse, int64_t tokens, int64_t vocab, int64_t k, float temperature,
+                        float* loss, void* stream);
+int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const int32_t* ids, const float* teacher,
+                        const float* teacher_lse, const float* dloss, int64_t tokens, int64_t vocab, int64_t k,
+                        float temperature, float* loss, void* dlogits, int grad_type, void* stream);
+
+/*
+ * nq_linear_cross_entropy_fwd, nq_linear_cross_entropy_bwd -- softmax cross entropy of a dense
+ * head, z = h W^T, without the logits in memory, and its gradients:
+ *     lse_i = log sum_v exp(z_iv),  loss_i = lse_i - z_i,labels[i],
+ *     dz_iv = dloss_i (exp(z_iv - lse_i) - [v = labels[i]]),  dh = dz W,  dW = dz^T h.
+ *   h       : tokens x d bfloat16;  W : vocab x d bfloat16 (one row per class)
+ *   labels  : tokens int32; a label outside 0 .. vocab-1 (e.g. -100) marks a token that does
+ *             not count: loss 0 and dz = 0 (its lse is written, and its h must be finite)
+ *   loss, lse : tokens float32 (written);  bwd reads lse as fwd wrote it
+ *   dloss   : tokens float32
+ *   dh : tokens x d bfloat16, dW : vocab x d bfloat16 (written; either may be NULL)
+ *   scratch : at least nq_linear_cross_entropy_scratch_bytes(tokens, vocab, d, backward) bytes
+ *             (scratch_bytes smaller: NQ_ERR_NOMEM), free again when the call's work is done
+ *   tokens : 0 .. 1<<24 (else NQ_ERR_BATCH; with 0, bwd writes dW with zeros);  vocab : 1 ..
+ *   1<<20;  d : a positive multiple of 8, at most 1<<20 (else NQ_ERR_SHAPE).
+ * Forward: products exact, sums fp32.  Backward: dz passes through bfloat16 (the operand type
+ * of the tensor cores beside h and W), sums over classes and tokens are fp32, results are
+ * rounded once to bfloat16: |error of dh_ij| <= 2^-8 (sum_v |dz_iv W_vj| + |dh_ij|), likewise
+ * dW.  The scratch of bwd is bounded: dz exists for a piece of the vocabulary at a time (at
+ * most 256 MB, or 128 classes), plus 4 tokens d bytes of sums when there is more than one
+ * piece.  Repeated calls agree bit for bit.  A bounded device wait that gave up is reported by
+ * nq_device_status.
+ */
+int64_t nq_linear_cross_entropy_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d, int backward);
+int nq_linear_cross_entropy_fwd(const void* h, const void* W, const int32_t* labels, int64_t tokens, int64_t vocab,
+                                int64_t d, float* loss, float* lse, void* scratch, int64_t scratch_bytes, void* stream);
+int nq_linear_cross_entropy_bwd(const void* h, const void* W, const int32_t* labels, const float* lse,
+                                const float* dloss, int64_t tokens, int64_t vocab, int64_t d, void* dh, void* dW,
+                                void* scratch, int64_t scratch_bytes, void* stream);
+
+/*
  * LB-ADMM initialiser of the binary factorisation (hardwired.dev, "NanoQuant jednoduse",
  * section "Trikrokovy pipeline", step 2 "Inicializace binarni faktorizace (LB-ADMM)": ADMM
  * alternating a closed-form least-squares solve for the continuous parameters with a
