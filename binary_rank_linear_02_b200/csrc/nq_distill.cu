@@ -219,29 +219,32 @@ __global__ void __launch_bounds__(kDtThreads) distill_kernel(const DistillArgs p
         if (owner[k]) l = join(l, MaxSum{sz[k], 1.f}, c);
     const float ml = block_reduce(l.m, red_f, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
     const float sl = block_reduce(l.s * ex2((l.m - or_zero(ml)) * c), red_f2, 0.f, [](float a, float b) { return a + b; });
-    const MaxSum all = join(MaxSum{mr, sr}, MaxSum{ml, sl}, c);
+    // their union: in fp64, since one exponential's error would shift every logarithm below
+    const float m = fmaxf(mr, ml);
+    const double sum = (mr > -INFINITY ? sr * exp(((double)mr - m) * invT) : 0.0) +
+                       (ml > -INFINITY ? sl * exp(((double)ml - m) * invT) : 0.0);
 
     const double qrest = whole && mr > -INFINITY ? fmax(0.0, 1.0 - qsum) : 0.0;
     if (p.loss) {
-        const double logsum = log((double)all.s);  // log p_v = (z_v - all.m) / T - logsum
+        const double logsum = log(sum);  // log p_v = (z_v - m) / T - logsum
         double part = 0.0;
         for (int k = tid; k < K; k += kDtThreads) {
             const double lq = (double)p.teacher[row * K + k] * invT - shift;
-            if (sid[k] >= 0 && sq[k] > 0.f) part += exp(lq) * (lq - (((double)sz[k] - all.m) * invT - logsum));
+            if (sid[k] >= 0 && sq[k] > 0.f) part += exp(lq) * (lq - (((double)sz[k] - m) * invT - logsum));
         }
         part = block_reduce(part, red_d, 0.0, [](double a, double b) { return a + b; });
         if (tid == 0) {
-            if (qrest > 0.0) part += qrest * (log(qrest) - (((double)mr - all.m) * invT + log((double)sr) - logsum));
+            if (qrest > 0.0) part += qrest * (log(qrest) - (((double)mr - m) * invT + log((double)sr) - logsum));
             p.loss[row] = (float)(part * (double)p.temperature * (double)p.temperature);
         }
     }
     if constexpr (kGrad) {
         // outside the list dz_v = 2^((z_v - mr) c) (tot 2^((mr - m) c) / sum - qrest / sr) T dloss
-        const float gT = p.temperature * p.dloss[row], tot = (float)(qsum + qrest);
+        const float gT = p.temperature * p.dloss[row];
         // (the two nearly cancel when the student is close: in fp64)
-        const float base = or_zero(mr), scale = tot * gT / all.s;
+        const float base = or_zero(mr), scale = (float)((qsum + qrest) * gT / sum);
         const float factor =
-            mr > -INFINITY ? (float)((exp(((double)mr - all.m) * invT) * (qsum + qrest) / all.s - qrest / sr) * gT) : 0.f;
+            mr > -INFINITY ? (float)((exp(((double)mr - m) * invT) * (qsum + qrest) / sum - qrest / sr) * gT) : 0.f;
         const bool aligned = (reinterpret_cast<uintptr_t>(dz + head) & 15) == 0;
         auto put1 = [&](int v) { store1(dz + v, ex2((load1(z + v) - base) * c) * factor); };
         if (tid < head) put1(tid);
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kDtThreads) distill_kernel(const DistillArgs p
                 for (int j = 0; j < K; ++j)
                     if (sid[j] == sid[k]) q += sq[j];
             }
-            store1(dz + sid[k], ex2((sz[k] - all.m) * c) * scale - q * gT);
+            store1(dz + sid[k], ex2((sz[k] - m) * c) * scale - q * gT);
         }
     }
 }

@@ -3,7 +3,7 @@
 //     z = h W^T,  lse_i = log sum_v exp(z_iv),  loss_i = lse_i - z_i,label(i),
 //     dz_iv = dloss_i (exp(z_iv - lse_i) - [v = label(i)]),  dh = dz W,  dW = dz^T h.
 //
-// The logits exist only as accumulators in tensor memory.  Forward: each 128 x 128 tile of z
+// The logits exist only as accumulators in tensor memory.  Forward: each 256 x 256 tile of z
 // is reduced in its epilogue to a maximum and a sum of exponentials per row (fp32), and a
 // second kernel joins a row's tiles in order.  Backward: the vocabulary is taken in pieces;
 // a piece's z is computed again, its epilogue writes dz as bfloat16 into a scratch of bounded
@@ -25,21 +25,25 @@
 namespace nq {
 namespace {
 
-constexpr int kXM = 128, kXN = 128, kXK = 64;
-constexpr int kXStages = 3;
-constexpr int kXTileBytes = kXM * kXK * 2;
+// A cluster of two CTAs computes a 256 x 256 tile: each holds 128 rows of A, 128 rows (or
+// columns) of B and the accumulators of its 128 rows.
+constexpr int kXHalfTile = 128, kXTile = 256, kXK = 64;
+constexpr int kXStages = 6;
+constexpr int kXTileBytes = kXHalfTile * kXK * 2;   // 16 KB of A, 16 KB of B per CTA and stage
 constexpr int kXStageBytes = 2 * kXTileBytes;
-constexpr int kXHalf = kXTileBytes / 2;  // one TMA box of an MN-major tile: 64 rows x 64 elements
+constexpr int kXHalf = kXTileBytes / 2;             // one TMA box of an MN-major tile: 64 rows x 64 elements
 constexpr int kXThreads = 192;
 constexpr int kXSmem = kXStages * kXStageBytes + 1024 + 1024;
+constexpr uint32_t kXTmemCols = 512;                // two accumulators of 256 columns
 constexpr int64_t kXPieceBytes = int64_t(256) << 20;  // scratch for dz
+constexpr int64_t kXSumBytes = int64_t(256) << 20;    // scratch for dh's partial sums
 
 // A device-side wait that gave up (NQ_ERR_TIMEOUT) is recorded here; nq_device_status reads it.
 __device__ unsigned g_xent_status;
 
 __host__ __device__ constexpr uint32_t xent_idesc(bool amn, bool bmn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((amn ? 1u : 0u) << 15) | ((bmn ? 1u : 0u) << 16) |
-           ((uint32_t)(kXN >> 3) << 17) | ((uint32_t)(kXM >> 4) << 24);
+           ((uint32_t)(kXTile >> 3) << 17) | ((uint32_t)(kXTile >> 4) << 24);
 }
 
 // SW128 MN-major operand descriptor: rows of 64 elements along K, 8-row groups 1024 B apart,
@@ -51,10 +55,47 @@ __device__ __forceinline__ uint64_t xent_desc_mn(uint32_t addr) {
 
 struct XentBarriers {
     unsigned long long full[kXStages], empty[kXStages];
-    unsigned long long tmem_full, drain;
+    unsigned long long acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
 };
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The address of this CTA's shared-memory location in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A load into this CTA's shared memory that reports its bytes to a barrier of the pair.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// Arrives on this barrier in both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 
 __device__ __forceinline__ float xent_ex2(float x) {
     float r;
@@ -63,7 +104,7 @@ __device__ __forceinline__ float xent_ex2(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum { kStats = 0, kDz = 1, kToBf16 = 2, kAccumulate = 3 };
+enum { kStats = 0, kDz = 1, kToBf16 = 2, kPartial = 3 };
 
 struct XentEpilogue {
     int64_t rows, cols;     // of the product (unpadded)
@@ -73,10 +114,10 @@ struct XentEpilogue {
     float* picked;          // kStats: z of the label, per row
     const float* lse;       // kDz
     const float* dloss;     // kDz
-    uint16_t* out;          // kDz, kToBf16, kAccumulate's last piece: bf16
-    float* acc;             // kAccumulate: fp32 sums, pitch = cols
+    uint16_t* out;          // kDz, kToBf16: bf16, rows ldo apart
     int64_t ldo;
-    int first, last;        // kAccumulate
+    float* part;            // kPartial: [split][row][cols] fp32, added to unless first
+    int first;
 };
 
 __device__ __forceinline__ uint32_t xent_pack(float lo, float hi) {
@@ -98,10 +139,72 @@ __device__ __forceinline__ void xent_store32(uint16_t* out, const float (&v)[32]
     }
 }
 
+// One row's 32 accumulators from column c0 of the tile's n0 on: what becomes of them.
+// `m`, `s` run over the tile's columns (kStats).
+template <int kEpi>
+__device__ __forceinline__ void xent_columns(const XentEpilogue& e, float (&v)[32], int64_t row, bool there, int64_t col,
+                                             int64_t split, int64_t label, float lse2, float dl, float& m, float& s) {
+    const int64_t left = e.cols - col;
+    const int n = left < 32 ? (int)(left < 0 ? 0 : left) : 32;
+    const int64_t at = label - e.label0 - col;  // the label's column in this block, if it is in it
+    if constexpr (kEpi == kStats) {
+        float mm = m;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (j >= n) v[j] = -INFINITY;
+            mm = fmaxf(mm, v[j]);
+            if (j == at && label >= 0) e.picked[row] = v[j];
+        }
+        const float f = mm == -INFINITY ? 0.f : mm;
+        s *= xent_ex2((m - f) * kLog2e);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s += xent_ex2((v[j] - f) * kLog2e);
+        m = mm;
+    } else if constexpr (kEpi == kDz) {
+        if (there && n > 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float q = xent_ex2(fmaf(v[j], kLog2e, -lse2)) - (j == at && label >= 0 ? 1.f : 0.f);
+                v[j] = dl != 0.f ? q * dl : 0.f;
+            }
+            xent_store32(e.out + row * e.ldo + col, v, n);
+        }
+    } else if constexpr (kEpi == kToBf16) {
+        if (there && n > 0) xent_store32(e.out + row * e.ldo + col, v, n);
+    } else {
+        if (there && n > 0) {  // cols is a multiple of 8: so is n
+            float* a = e.part + (split * e.rows + row) * e.cols + col;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                if (j >= n) continue;
+                float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                if (!e.first) {
+                    const float4 o = *reinterpret_cast<const float4*>(a + j);
+                    w.x += o.x;
+                    w.y += o.y;
+                    w.z += o.z;
+                    w.w += o.w;
+                }
+                *reinterpret_cast<float4*>(a + j) = w;
+            }
+        }
+    }
+}
+
+// How the work is cut: tiles of the product, K blocks per share of the sum, shares.
+struct XentPlan {
+    int tm, tn, nkb, per_split, splits;
+    int n_fastest;  // the order of the tiles: neighbours in the first index run at the same time
+};
+
+// A persistent pair of CTAs per two SMs walks over the tiles.  Warp 0 loads (each CTA its own
+// halves of A and B, reporting to the first CTA's barriers), warp 1 of the first CTA issues the
+// MMAs of both, warps 2-5 of each CTA take the accumulators of its 128 rows out of tensor
+// memory while the next tile's are being summed in the other 256 columns.
 template <int kEpi, bool AMN, bool BMN>
-__global__ void __launch_bounds__(kXThreads, 2)
-xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, int nkb,
-                 const XentEpilogue e) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
+xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                 const XentPlan plan, const XentEpilogue e) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -109,91 +212,136 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
     volatile int* abort_flag = &bar.abort_flag;
     unsigned* status = &g_xent_status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m0 = blockIdx.x * kXM, n0 = blockIdx.y * kXN;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int tiles = plan.tm * plan.tn, items = tiles * plan.splits;
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < kXStages; ++st) {
             mbar_init(smem_u32(&bar.full[st]), 1);
             mbar_init(smem_u32(&bar.empty[st]), 1);
         }
-        mbar_init(smem_u32(&bar.tmem_full), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar.acc_full[i]), 1);
+            mbar_init(smem_u32(&bar.acc_empty[i]), 8);  // the epilogue warps of both CTAs
+        }
         mbar_init(smem_u32(&bar.drain), 1);
         bar.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_u32(&bar.tmem_base)), "r"((uint32_t)kXN));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&bar.tmem_base)), "r"(kXTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bar.tmem_base;
     pdl_wait();
+    pdl_trigger();
+
+    auto tile_of = [&](int item, int& tm, int& tn, int& kb0, int& kb1) {
+        const int split = item / tiles, tile = item % tiles;
+        if (plan.n_fastest) {
+            tm = tile / plan.tn;
+            tn = tile % plan.tn;
+        } else {
+            tn = tile / plan.tm;
+            tm = tile % plan.tm;
+        }
+        kb0 = split * plan.per_split;
+        kb1 = kb0 + plan.per_split < plan.nkb ? kb0 + plan.per_split : plan.nkb;
+        return split;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
-            int issued = 0;
-            for (int kb = 0; kb < nkb; ++kb) {
-                const int st = kb % kXStages;
-                const uint32_t ph = (uint32_t)(kb / kXStages) & 1u;
-                if (!mbar_wait(smem_u32(&bar.empty[st]), ph ^ 1u, abort_flag, status)) break;
-                const uint32_t full = smem_u32(&bar.full[st]);
-                mbar_expect_tx(full, (uint32_t)kXStageBytes);
-                const uint32_t dst = base + (uint32_t)(st * kXStageBytes);
-                if constexpr (AMN) {
-                    tma_load_2d(dst, &amap, m0, kb * kXK, full);
-                    tma_load_2d(dst + kXHalf, &amap, m0 + 64, kb * kXK, full);
-                } else {
-                    tma_load_2d(dst, &amap, kb * kXK, m0, full);
+            fence_proxy_async_global();  // dz was written by ordinary stores of the kernel before
+            int it = 0;  // K blocks so far
+            bool ok = true;
+            for (int item = pair; item < items && ok; item += pairs) {
+                int tm, tn, kb0, kb1;
+                tile_of(item, tm, tn, kb0, kb1);
+                const int m0 = tm * kXTile + (int)rank * kXHalfTile, n0 = tn * kXTile + (int)rank * kXHalfTile;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int st = it % kXStages;
+                    const uint32_t ph = (uint32_t)(it / kXStages) & 1u;
+                    if (!mbar_wait(smem_u32(&bar.empty[st]), ph ^ 1u, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = in_leader(smem_u32(&bar.full[st]));
+                    if (rank == 0) mbar_expect_tx(smem_u32(&bar.full[st]), 2u * kXStageBytes);
+                    const uint32_t dst = base + (uint32_t)(st * kXStageBytes);
+                    if constexpr (AMN) {
+                        pair_load_2d(dst, &amap, m0, kb * kXK, full);
+                        pair_load_2d(dst + kXHalf, &amap, m0 + 64, kb * kXK, full);
+                    } else {
+                        pair_load_2d(dst, &amap, kb * kXK, m0, full);
+                    }
+                    if constexpr (BMN) {
+                        pair_load_2d(dst + kXTileBytes, &bmap, n0, kb * kXK, full);
+                        pair_load_2d(dst + kXTileBytes + kXHalf, &bmap, n0 + 64, kb * kXK, full);
+                    } else {
+                        pair_load_2d(dst + kXTileBytes, &bmap, kb * kXK, n0, full);
+                    }
                 }
-                if constexpr (BMN) {
-                    tma_load_2d(dst + kXTileBytes, &bmap, n0, kb * kXK, full);
-                    tma_load_2d(dst + kXTileBytes + kXHalf, &bmap, n0 + 64, kb * kXK, full);
-                } else {
-                    tma_load_2d(dst + kXTileBytes, &bmap, kb * kXK, n0, full);
-                }
-                ++issued;
             }
-            if (*abort_flag) {
-                for (int kb = issued - kXStages < 0 ? 0 : issued - kXStages; kb < issued; ++kb)
-                    mbar_drain(smem_u32(&bar.full[kb % kXStages]), (uint32_t)(kb / kXStages) & 1u);
-            }
+            // given up: what the pair has in flight reports to the first CTA's barriers
+            if (!ok && rank == 0)
+                for (int i = it < kXStages ? 0 : it - kXStages; i < it; ++i)
+                    mbar_drain(smem_u32(&bar.full[i % kXStages]), (uint32_t)(i / kXStages) & 1u);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             constexpr uint32_t idesc = xent_idesc(AMN, BMN);
-            int kb = 0;
-            for (; kb < nkb; ++kb) {
-                const int st = kb % kXStages;
-                const uint32_t ph = (uint32_t)(kb / kXStages) & 1u;
-                if (!mbar_wait(smem_u32(&bar.full[st]), ph, abort_flag, status)) break;
+            int it = 0, n = 0;
+            bool ok = true;
+            for (int item = pair; item < items && ok; item += pairs, ++n) {
+                int tm, tn, kb0, kb1;
+                tile_of(item, tm, tn, kb0, kb1);
+                const int acc = n & 1;
+                if (!mbar_wait(smem_u32(&bar.acc_empty[acc]), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, status)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
-                const uint32_t aaddr = base + (uint32_t)(st * kXStageBytes), baddr = aaddr + kXTileBytes;
-                const uint64_t ad = AMN ? xent_desc_mn(aaddr) : sw128_desc(aaddr);
-                const uint64_t bd = BMN ? xent_desc_mn(baddr) : sw128_desc(baddr);
-                constexpr uint64_t astep = AMN ? 2048 / 16 : 32 / 16, bstep = BMN ? 2048 / 16 : 32 / 16;
+                const uint32_t d = tmem + (uint32_t)(acc * kXTile);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int st = it % kXStages;
+                    if (!mbar_wait(smem_u32(&bar.full[st]), (uint32_t)(it / kXStages) & 1u, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t aaddr = base + (uint32_t)(st * kXStageBytes), baddr = aaddr + kXTileBytes;
+                    const uint64_t ad = AMN ? xent_desc_mn(aaddr) : sw128_desc(aaddr);
+                    const uint64_t bd = BMN ? xent_desc_mn(baddr) : sw128_desc(baddr);
+                    constexpr uint64_t astep = AMN ? 2048 / 16 : 32 / 16, bstep = BMN ? 2048 / 16 : 32 / 16;
 #pragma unroll
-                for (int k = 0; k < kXK / 16; ++k)
-                    umma_f16(tmem, ad + (uint64_t)k * astep, bd + (uint64_t)k * bstep, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                umma_commit(smem_u32(&bar.empty[st]));
+                    for (int k = 0; k < kXK / 16; ++k)
+                        pair_mma(d, ad + (uint64_t)k * astep, bd + (uint64_t)k * bstep, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
+                    pair_commit(smem_u32(&bar.empty[st]));
+                }
+                if (ok) pair_commit(smem_u32(&bar.acc_full[acc]));
             }
-            if (kb == nkb) {
-                umma_commit(smem_u32(&bar.tmem_full));
-            } else {
-                umma_commit(smem_u32(&bar.drain));
+            if (!ok) {
+                pair_commit(smem_u32(&bar.drain));
                 mbar_drain(smem_u32(&bar.drain), 0);
             }
         }
     } else {
-        if (mbar_wait(smem_u32(&bar.tmem_full), 0, abort_flag, status)) {
-            tc_fence_after();
-            pdl_trigger();
-            const int quad = warp & 3;
-            const int64_t row = m0 + quad * 32 + lane;
+        const int quad = warp & 3;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        int n = 0;
+        for (int item = pair; item < items; item += pairs, ++n) {
+            int tm, tn, kb0, kb1;
+            const int split = tile_of(item, tm, tn, kb0, kb1);
+            const int acc = n & 1;
+            const int64_t row = (int64_t)tm * kXTile + (int)rank * kXHalfTile + quad * 32 + lane;
             const bool there = row < e.rows;
-            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16);
             int64_t label = -1;
             float lse2 = 0.f, dl = 0.f;
             if constexpr (kEpi == kStats || kEpi == kDz) {
@@ -204,69 +352,51 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                 lse2 = there ? e.lse[row] * kLog2e : 0.f;
                 dl = there && label >= 0 ? e.dloss[row] : 0.f;
             }
+            if (!mbar_wait(smem_u32(&bar.acc_full[acc]), (uint32_t)(n >> 1) & 1u, abort_flag, status)) break;
+            tc_fence_after();
             float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-            for (int c0 = 0; c0 < kXN; c0 += 32) {
+            for (int c0 = 0; c0 < kXTile; c0 += 32) {
                 uint32_t w[32];
-                tmem_ld32(taddr + (uint32_t)c0, w);
+                tmem_ld32(tmem + lanes + (uint32_t)(acc * kXTile + c0), w);
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
-                const int64_t left = e.cols - n0 - c0;
-                const int n = left < 32 ? (int)(left < 0 ? 0 : left) : 32;
-                const int64_t at = label - e.label0 - n0 - c0;  // the label's column in this block, if it is in it
-                if constexpr (kEpi == kStats) {
-                    float mm = m;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (j >= n) v[j] = -INFINITY;
-                        mm = fmaxf(mm, v[j]);
-                        if (j == at && label >= 0) e.picked[row] = v[j];
-                    }
-                    const float f = mm == -INFINITY ? 0.f : mm;
-                    s *= xent_ex2((m - f) * kLog2e);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) s += xent_ex2((v[j] - f) * kLog2e);
-                    m = mm;
-                } else if constexpr (kEpi == kDz) {
-                    if (there) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float q = xent_ex2(fmaf(v[j], kLog2e, -lse2)) - (j == at && label >= 0 ? 1.f : 0.f);
-                            v[j] = dl != 0.f ? q * dl : 0.f;
-                        }
-                        xent_store32(e.out + row * e.ldo + n0 + c0, v, n);
-                    }
-                } else if constexpr (kEpi == kToBf16) {
-                    if (there) xent_store32(e.out + row * e.ldo + n0 + c0, v, n);
-                } else {
-                    if (there) {
-                        float* a = e.acc + row * e.cols + n0 + c0;
-                        if (!e.first) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j < n) v[j] += a[j];
-                        }
-                        if (e.last) {
-                            xent_store32(e.out + row * e.ldo + n0 + c0, v, n);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j < n) a[j] = v[j];
-                        }
-                    }
-                }
+                xent_columns<kEpi>(e, v, row, there, (int64_t)tn * kXTile + c0, split, label, lse2, dl, m, s);
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(in_leader(smem_u32(&bar.acc_empty[acc])));
             if constexpr (kEpi == kStats) {
-                if (there) e.stats[(int64_t)blockIdx.y * e.rows + row] = make_float2(m, s);
+                if (there) e.stats[(int64_t)tn * e.rows + row] = make_float2(m, s);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still signal it
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)kXN));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kXTmemCols));
+    }
+}
+
+// dh = the shares' sums, added in order, as bf16 (four at a time: cols is a multiple of 8).
+__global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__ part, int splits, int64_t count,
+                                                       uint16_t* __restrict__ out) {
+    pdl_wait();
+    for (int64_t i = 4 * (blockIdx.x * (int64_t)blockDim.x + threadIdx.x); i < count;
+         i += 4 * (int64_t)gridDim.x * blockDim.x) {
+        float4 a = *reinterpret_cast<const float4*>(part + i);
+        for (int q = 1; q < splits; ++q) {
+            const float4 b = *reinterpret_cast<const float4*>(part + q * count + i);
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+        }
+        *reinterpret_cast<uint2*>(out + i) = make_uint2(xent_pack(a.x, a.y), xent_pack(a.z, a.w));
     }
 }
 
@@ -326,9 +456,12 @@ bool xent_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+int64_t cut(int64_t v, int64_t a) { return (v + a - 1) / a; }
+
 template <int kEpi, bool AMN, bool BMN>
 int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K,
-                const XentEpilogue& e, cudaStream_t stream) {
+                int splits, bool n_fastest, const XentEpilogue& e, cudaStream_t stream) {
     static unsigned long long init_mask = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NQ_ERR_CUDA;
@@ -340,50 +473,89 @@ int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, 
         __atomic_fetch_or(&init_mask, bit, __ATOMIC_RELEASE);
     }
     CUtensorMap amap, bmap;
-    if (!(AMN ? xent_map(&amap, A, K, M, lda, 64) : xent_map(&amap, A, M, K, lda, kXM)) ||
-        !(BMN ? xent_map(&bmap, B, K, N, ldb, 64) : xent_map(&bmap, B, N, K, ldb, kXN)))
+    if (!(AMN ? xent_map(&amap, A, K, M, lda, kXK) : xent_map(&amap, A, M, K, lda, kXHalfTile)) ||
+        !(BMN ? xent_map(&bmap, B, K, N, ldb, kXK) : xent_map(&bmap, B, N, K, ldb, kXHalfTile)))
         return NQ_ERR_CUDA;
-    const dim3 grid((unsigned)((M + kXM - 1) / kXM), (unsigned)((N + kXN - 1) / kXN));
-    return launch_pdl(xent_gemm_kernel<kEpi, AMN, BMN>, grid, dim3(kXThreads), (size_t)kXSmem, stream, amap, bmap,
-                      (int)((K + kXK - 1) / kXK), e) == cudaSuccess
+    XentPlan plan;
+    plan.tm = (int)cut(M, kXTile);
+    plan.tn = (int)cut(N, kXTile);
+    plan.nkb = (int)cut(K, kXK);
+    plan.per_split = (int)cut(plan.nkb, splits);
+    plan.splits = splits;
+    plan.n_fastest = n_fastest;
+    const int64_t items = (int64_t)plan.tm * plan.tn * splits, pairs = sm_count() / 2;
+    return launch_pdl(xent_gemm_kernel<kEpi, AMN, BMN>, dim3((unsigned)(2 * (items < pairs ? items : pairs))),
+                      dim3(kXThreads), (size_t)kXSmem, stream, amap, bmap, plan, e) == cudaSuccess
                ? NQ_OK
                : NQ_ERR_CUDA;
 }
 
-int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-int64_t tiles_n(int64_t v) { return (v + kXN - 1) / kXN; }
-
 // Classes per piece of the backward: as many whole column tiles as dz's scratch holds.
 int64_t piece_classes(int64_t tokens, int64_t vocab) {
-    const int64_t fit = kXPieceBytes / (2 * tokens) / kXN * kXN;
-    const int64_t all = round_up(vocab, kXN);
-    return fit < kXN ? kXN : fit < all ? fit : all;
+    const int64_t fit = kXPieceBytes / (2 * tokens) / kXTile * kXTile;
+    const int64_t all = round_up(vocab, kXTile);
+    return fit < kXTile ? kXTile : fit < all ? fit : all;
+}
+
+// Shares of dh's sum over the classes of a piece: the count whose waves of tiles over the pairs
+// of SMs take the least time, a K block (64 classes) being the unit and the traffic of the
+// shares' sums (4 bytes written and read again per element, about 1.2 MB in the time of a K
+// block) added; no share is empty and all fit their scratch.
+int dh_splits(int64_t tokens, int64_t classes, int64_t d) {
+    const int64_t tiles = cut(tokens, kXTile) * cut(d, kXTile), nkb = cut(classes, kXK), pairs = sm_count() / 2;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int64_t s = 1; s <= 16 && s <= nkb; ++s) {
+        if (s > 1 && 4 * s * tokens * d > kXSumBytes) break;
+        const int64_t per = cut(nkb, s);
+        if (cut(nkb, per) != s) continue;
+        const int64_t time = cut(tiles * s, pairs) * (per + 8) + (s > 1 ? 8 * s * tokens * d / 1200000 : 0);
+        if (time < least) {
+            least = time;
+            best = (int)s;
+        }
+    }
+    return best;
+}
+
+struct BackwardPlan {
+    int64_t piece;
+    int splits;
+    bool direct;  // one piece and one share: dh straight to bf16
+};
+BackwardPlan plan_backward(int64_t tokens, int64_t vocab, int64_t d) {
+    BackwardPlan p;
+    p.piece = piece_classes(tokens, vocab);
+    p.splits = dh_splits(tokens, p.piece < vocab ? p.piece : vocab, d);
+    p.direct = p.piece >= vocab && p.splits == 1;
+    return p;
 }
 
 }  // namespace
 
 int64_t xent_fwd_scratch_bytes(int64_t tokens, int64_t vocab) {
-    return round_up(8 * tokens * tiles_n(vocab), 256) + round_up(4 * tokens, 256);
+    return round_up(8 * tokens * cut(vocab, kXTile), 256) + round_up(4 * tokens, 256);
 }
 
 int64_t xent_bwd_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d) {
-    const int64_t piece = piece_classes(tokens, vocab);
-    return round_up(2 * tokens * piece, 256) + (piece < vocab ? round_up(4 * tokens * d, 256) : 0);
+    const BackwardPlan p = plan_backward(tokens, vocab, d);
+    return round_up(2 * tokens * p.piece, 256) + (p.direct ? 0 : round_up(4 * p.splits * tokens * d, 256));
 }
 
 int xent_forward(const uint16_t* h, const uint16_t* W, const int32_t* labels, int64_t tokens, int64_t vocab, int64_t d,
                  float* loss, float* lse, void* scratch, cudaStream_t stream) {
+    const int64_t tiles = cut(vocab, kXTile);
     XentEpilogue e = {};
     e.rows = tokens;
     e.cols = e.vocab = vocab;
     e.labels = labels;
     e.stats = static_cast<float2*>(scratch);
-    e.picked = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(8 * tokens * tiles_n(vocab), 256));
-    const int rc = xent_launch<kStats, false, false>(h, d, W, d, tokens, vocab, d, e, stream);
+    e.picked = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(8 * tokens * tiles, 256));
+    const int rc = xent_launch<kStats, false, false>(h, d, W, d, tokens, vocab, d, 1, false, e, stream);
     if (rc != NQ_OK) return rc;
     return launch_pdl(xent_join_kernel, dim3((unsigned)((tokens + 7) / 8)), dim3(256), 0, stream,
-                      (const float2*)e.stats, (const float*)e.picked, labels, tokens, vocab, (int)tiles_n(vocab), loss,
-                      lse) == cudaSuccess
+                      (const float2*)e.stats, (const float*)e.picked, labels, tokens, vocab, (int)tiles, loss, lse) ==
+                   cudaSuccess
                ? NQ_OK
                : NQ_ERR_CUDA;
 }
@@ -391,9 +563,10 @@ int xent_forward(const uint16_t* h, const uint16_t* W, const int32_t* labels, in
 int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, const float* lse, const float* dloss,
                   int64_t tokens, int64_t vocab, int64_t d, uint16_t* dh, uint16_t* dW, void* scratch,
                   cudaStream_t stream) {
-    const int64_t piece = piece_classes(tokens, vocab);
+    const BackwardPlan plan = plan_backward(tokens, vocab, d);
+    const int64_t piece = plan.piece;
     uint16_t* dz = static_cast<uint16_t*>(scratch);
-    float* acc = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(2 * tokens * piece, 256));
+    float* part = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(2 * tokens * piece, 256));
     for (int64_t v0 = 0; v0 < vocab; v0 += piece) {
         const int64_t nv = vocab - v0 < piece ? vocab - v0 : piece;
         XentEpilogue e = {};
@@ -406,7 +579,7 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
         e.dloss = dloss;
         e.out = dz;
         e.ldo = piece;
-        int rc = xent_launch<kDz, false, false>(h, d, W + v0 * d, d, tokens, nv, d, e, stream);
+        int rc = xent_launch<kDz, false, false>(h, d, W + v0 * d, d, tokens, nv, d, 1, false, e, stream);
         if (rc != NQ_OK) return rc;
         if (dW) {
             XentEpilogue g = {};
@@ -414,21 +587,33 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
             g.cols = d;
             g.out = dW + v0 * d;
             g.ldo = d;
-            rc = xent_launch<kToBf16, true, true>(dz, piece, h, d, nv, d, tokens, g, stream);
+            rc = xent_launch<kToBf16, true, true>(dz, piece, h, d, nv, d, tokens, 1, true, g, stream);
             if (rc != NQ_OK) return rc;
         }
         if (dh) {
             XentEpilogue g = {};
             g.rows = tokens;
             g.cols = d;
-            g.out = dh;
-            g.ldo = d;
-            g.acc = acc;
-            g.first = v0 == 0;
-            g.last = v0 + piece >= vocab;
-            rc = xent_launch<kAccumulate, false, true>(dz, piece, W + v0 * d, d, tokens, d, nv, g, stream);
+            if (plan.direct) {
+                g.out = dh;
+                g.ldo = d;
+                rc = xent_launch<kToBf16, false, true>(dz, piece, W + v0 * d, d, tokens, d, nv, 1, false, g, stream);
+            } else {
+                // the last piece may have fewer K blocks than shares: then it adds to the first ones
+                g.part = part;
+                g.first = v0 == 0;
+                const int64_t nkb = cut(nv, kXK), per = cut(nkb, plan.splits);
+                rc = xent_launch<kPartial, false, true>(dz, piece, W + v0 * d, d, tokens, d, nv, (int)cut(nkb, per), false,
+                                                        g, stream);
+            }
             if (rc != NQ_OK) return rc;
         }
+    }
+    if (dh && !plan.direct) {
+        const int64_t count = tokens * d, blocks = cut(count, 1024), cap = 16 * (int64_t)sm_count();
+        if (launch_pdl(xent_sum_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, stream,
+                       (const float*)part, plan.splits, count, dh) != cudaSuccess)
+            return NQ_ERR_CUDA;
     }
     return NQ_OK;
 }
