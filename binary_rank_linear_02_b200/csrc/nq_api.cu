@@ -829,9 +829,12 @@ int nq_device_status(void* stream) {
     unsigned word = 0;
     if (cudaMemcpy(&word, ws->status + 1, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess) return NQ_ERR_CUDA;
     if (word != 0 && cudaMemset(ws->status + 1, 0, sizeof(unsigned)) != cudaSuccess) return NQ_ERR_CUDA;
-    unsigned head = 0;  // the cross entropy's kernels have a word of their own
-    if (xent_take_status(&head) != NQ_OK) return NQ_ERR_CUDA;
-    if (word == 0 && head != 0) return -(int)head;
+    // the 4-bit products and the cross entropy have words of their own
+    for (auto take : {q4_take_status, xent_take_status}) {
+        unsigned head = 0;
+        if (take(&head) != NQ_OK) return NQ_ERR_CUDA;
+        if (word == 0) word = head;
+    }
     // a kernel that gave up may have left arrival counters part-way: start them from zero again
     if (word != 0 && cudaMemset(ws->counters, 0, sizeof(int) * (ws->counter_cap + 1)) != cudaSuccess)
         return NQ_ERR_CUDA;

@@ -177,7 +177,8 @@ int xent_forward(const uint16_t* h, const uint16_t* W, const int32_t* labels, in
 int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, const float* lse, const float* dloss,
                   int64_t tokens, int64_t vocab, int64_t d, uint16_t* dh, uint16_t* dW, void* scratch,
                   cudaStream_t stream);
-// reads and clears the status word of the cross entropy's kernels (the device is idle)
+// read and clear the status words of these kernels (the device is idle)
+int q4_take_status(unsigned* word);
 int xent_take_status(unsigned* word);
 
 }  // namespace nq

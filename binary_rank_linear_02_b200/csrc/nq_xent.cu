@@ -25,15 +25,15 @@
 namespace nq {
 namespace {
 
-// A cluster of two CTAs computes a 256 x 256 tile: each holds 128 rows of A, 128 rows (or
-// columns) of B and the accumulators of its 128 rows.
+// A cluster of two CTAs computes a tile of 256 rows and up to 256 columns: each holds 128 rows
+// of A, half of B's columns and the accumulators of its 128 rows.
 constexpr int kXHalfTile = 128, kXTile = 256, kXK = 64;
-constexpr int kXStages = 6;
-constexpr int kXTileBytes = kXHalfTile * kXK * 2;   // 16 KB of A, 16 KB of B per CTA and stage
-constexpr int kXStageBytes = 2 * kXTileBytes;
-constexpr int kXHalf = kXTileBytes / 2;             // one TMA box of an MN-major tile: 64 rows x 64 elements
+constexpr int kXABytes = kXHalfTile * kXK * 2;      // 16 KB of A per CTA and stage; B: 64 bytes per column of the tile
+constexpr int kXBox = 64 * kXK * 2;                 // one TMA box of an MN-major tile: 64 rows x 64 elements
+constexpr int kXMaxStages = 13;
 constexpr int kXThreads = 192;
-constexpr int kXSmem = kXStages * kXStageBytes + 1024 + 1024;
+constexpr int kXStageSpace = 224 * 1024;
+constexpr int kXSmem = kXStageSpace + 1024 + 1024;
 constexpr uint32_t kXTmemCols = 512;                // two accumulators of 256 columns
 constexpr int64_t kXPieceBytes = int64_t(256) << 20;  // scratch for dz
 constexpr int64_t kXSumBytes = int64_t(256) << 20;    // scratch for dh's partial sums
@@ -41,20 +41,20 @@ constexpr int64_t kXSumBytes = int64_t(256) << 20;    // scratch for dh's partia
 // A device-side wait that gave up (NQ_ERR_TIMEOUT) is recorded here; nq_device_status reads it.
 __device__ unsigned g_xent_status;
 
-__host__ __device__ constexpr uint32_t xent_idesc(bool amn, bool bmn) {
+__device__ __forceinline__ uint32_t xent_idesc(bool amn, bool bmn, int columns) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((amn ? 1u : 0u) << 15) | ((bmn ? 1u : 0u) << 16) |
-           ((uint32_t)(kXTile >> 3) << 17) | ((uint32_t)(kXTile >> 4) << 24);
+           ((uint32_t)(columns >> 3) << 17) | ((uint32_t)(kXTile >> 4) << 24);
 }
 
 // SW128 MN-major operand descriptor: rows of 64 elements along K, 8-row groups 1024 B apart,
 // the next 64 elements of M (or N) one box further.
 __device__ __forceinline__ uint64_t xent_desc_mn(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(kXHalf >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(kXBox >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
 struct XentBarriers {
-    unsigned long long full[kXStages], empty[kXStages];
+    unsigned long long full[kXMaxStages], empty[kXMaxStages];
     unsigned long long acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -106,17 +106,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 enum { kStats = 0, kDz = 1, kToBf16 = 2, kPartial = 3 };
 
+// "Token" and "class" in a transposed product (kT) change places: rows are classes (or
+// elements of d), columns are tokens.
 struct XentEpilogue {
     int64_t rows, cols;     // of the product (unpadded)
-    const int32_t* labels;  // kStats, kDz: per row
-    int64_t label0, vocab;  // first class of the columns; all classes
-    float2* stats;          // kStats: [column tile][row]: maximum, sum of exp(z - maximum)
-    float* picked;          // kStats: z of the label, per row
-    const float* lse;       // kDz
-    const float* dloss;     // kDz
-    uint16_t* out;          // kDz, kToBf16: bf16, rows ldo apart
+    const int32_t* labels;  // kStats, kDz: per token
+    int64_t label0, vocab;  // first class of the product; all classes
+    float2* stats;          // kStats: [slot][token]: maximum, sum of exp(z - maximum)
+    float* picked;          // kStats: z of the label, per token
+    const float* lse;       // kDz, per token
+    const float* dloss;     // kDz, per token
+    uint16_t* out;          // kDz, kToBf16: bf16, [row][column] with pitch ldo (kT: [column][row])
     int64_t ldo;
-    float* part;            // kPartial: [split][row][cols] fp32, added to unless first
+    float* part;            // kPartial: [split][row][column] fp32 (kT: [split][column][row]), added to unless first
     int first;
 };
 
@@ -125,67 +127,144 @@ __device__ __forceinline__ uint32_t xent_pack(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// 32 values of a row as bf16 at out[0 .. 31], the first n of them (out 16-byte aligned when whole).
+// 32 values of a row as bf16 at out[0 .. 31], the first n of them.
 __device__ __forceinline__ void xent_store32(uint16_t* out, const float (&v)[32], int n) {
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8)
+    for (int j = 0; j < 32; j += 8) {
+        if (aligned && j + 8 <= n) {
             *reinterpret_cast<uint4*>(out + j) = make_uint4(xent_pack(v[j], v[j + 1]), xent_pack(v[j + 2], v[j + 3]),
                                                             xent_pack(v[j + 4], v[j + 5]), xent_pack(v[j + 6], v[j + 7]));
-    } else {
+        } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < n) out[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+            for (int i = j; i < j + 8; ++i)
+                if (i < n) out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+        }
     }
 }
 
-// One row's 32 accumulators from column c0 of the tile's n0 on: what becomes of them.
-// `m`, `s` run over the tile's columns (kStats).
+// What a lane needs to know of a token: its label (-1: it does not count), the softmax's norm
+// (times log2 e) and the loss's weight.
+struct XentToken {
+    int label;
+    float lse2, dl;
+};
 template <int kEpi>
-__device__ __forceinline__ void xent_columns(const XentEpilogue& e, float (&v)[32], int64_t row, bool there, int64_t col,
-                                             int64_t split, int64_t label, float lse2, float dl, float& m, float& s) {
-    const int64_t left = e.cols - col;
-    const int n = left < 32 ? (int)(left < 0 ? 0 : left) : 32;
-    const int64_t at = label - e.label0 - col;  // the label's column in this block, if it is in it
-    if constexpr (kEpi == kStats) {
-        float mm = m;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j >= n) v[j] = -INFINITY;
-            mm = fmaxf(mm, v[j]);
-            if (j == at && label >= 0) e.picked[row] = v[j];
+__device__ __forceinline__ XentToken xent_token(const XentEpilogue& e, int64_t token, bool there) {
+    XentToken t{-1, 0.f, 0.f};
+    if constexpr (kEpi == kStats || kEpi == kDz) {
+        if (there) {
+            t.label = e.labels[token];
+            if (t.label < 0 || t.label >= e.vocab) t.label = -1;
+            if constexpr (kEpi == kDz) {
+                t.lse2 = e.lse[token] * kLog2e;
+                t.dl = t.label >= 0 ? e.dloss[token] : 0.f;
+            }
         }
-        const float f = mm == -INFINITY ? 0.f : mm;
-        s *= xent_ex2((m - f) * kLog2e);
+    }
+    return t;
+}
+
+__device__ __forceinline__ float xent_dz(float z, bool is_label, float lse2, float dl) {
+    const float q = xent_ex2(fmaf(z, kLog2e, -lse2)) - (is_label ? 1.f : 0.f);
+    return dl != 0.f ? q * dl : 0.f;
+}
+
+// Lane j's result: op over the lanes' v[j] (the lanes trade halves of what they hold: 31 shuffles).
+template <typename Op>
+__device__ __forceinline__ float across_lanes(const float (&values)[32], int lane, Op op) {
+    float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s += xent_ex2((v[j] - f) * kLog2e);
-        m = mm;
-    } else if constexpr (kEpi == kDz) {
-        if (there && n > 0) {
+    for (int i = 0; i < 32; ++i) v[i] = values[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + o], o);
+            v[i] = op(upper ? v[i + o] : v[i], other);
+        }
+    }
+    return v[0];
+}
+
+// 32 columns (from `col` on, n of them in the product) of the warp's 32 rows; lane = row.
+// tok: of the row (kT: of column col + lane); m, s run over the tile's columns (kStats).
+template <int kEpi, bool kT>
+__device__ __forceinline__ void xent_columns(const XentEpilogue& e, float (&v)[32], int64_t row, int64_t col, int n,
+                                             int64_t split, int64_t slot, const XentToken& tok, float& m, float& s) {
+    const bool there = row < e.rows;
+    const int lane = threadIdx.x & 31;
+    if constexpr (!kT) {
+        const int64_t at = tok.label - e.label0 - col;  // the label's column in this block, if it is in it
+        const bool counts = tok.label >= 0;
+        if constexpr (kEpi == kStats) {
+            float mm = m;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                const float q = xent_ex2(fmaf(v[j], kLog2e, -lse2)) - (j == at && label >= 0 ? 1.f : 0.f);
-                v[j] = dl != 0.f ? q * dl : 0.f;
+                if (j >= n) v[j] = -INFINITY;
+                mm = fmaxf(mm, v[j]);
+                if (j == at && j < n && counts) e.picked[row] = v[j];
+            }
+            const float f = mm == -INFINITY ? 0.f : mm;
+            s *= xent_ex2((m - f) * kLog2e);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s += xent_ex2((v[j] - f) * kLog2e);
+            m = mm;
+        } else if constexpr (kEpi == kPartial) {
+            if (there) {  // cols is a multiple of 8: so is n
+                float* a = e.part + (split * e.rows + row) * e.cols + col;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    if (j >= n) continue;
+                    float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    if (!e.first) {
+                        const float4 o = *reinterpret_cast<const float4*>(a + j);
+                        w.x += o.x;
+                        w.y += o.y;
+                        w.z += o.z;
+                        w.w += o.w;
+                    }
+                    *reinterpret_cast<float4*>(a + j) = w;
+                }
+            }
+        } else if (there) {
+            if constexpr (kEpi == kDz) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = xent_dz(v[j], j == at && counts, tok.lse2, tok.dl);
             }
             xent_store32(e.out + row * e.ldo + col, v, n);
         }
-    } else if constexpr (kEpi == kToBf16) {
-        if (there && n > 0) xent_store32(e.out + row * e.ldo + col, v, n);
     } else {
-        if (there && n > 0) {  // cols is a multiple of 8: so is n
-            float* a = e.part + (split * e.rows + row) * e.cols + col;
+        const int64_t cls = e.label0 + row;
+        if constexpr (kEpi == kStats) {
+            // the warp's 32 classes: per token a maximum and a sum
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                if (j >= n) continue;
-                float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                if (!e.first) {
-                    const float4 o = *reinterpret_cast<const float4*>(a + j);
-                    w.x += o.x;
-                    w.y += o.y;
-                    w.z += o.z;
-                    w.w += o.w;
+            for (int j = 0; j < 32; ++j) {
+                if (j >= n || !there) v[j] = -INFINITY;
+                if (__shfl_sync(0xffffffffu, tok.label, j) == cls && there && j < n) e.picked[col + j] = v[j];
+            }
+            const float top = across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
+            const float f = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = xent_ex2((v[j] - __shfl_sync(0xffffffffu, f, j)) * kLog2e);
+            const float sum = across_lanes(v, lane, [](float a, float b) { return a + b; });
+            if (lane < n) e.stats[slot * e.cols + col + lane] = make_float2(top, sum);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                float x = v[j];
+                if constexpr (kEpi == kDz)
+                    x = xent_dz(x, __shfl_sync(0xffffffffu, tok.label, j) == cls, __shfl_sync(0xffffffffu, tok.lse2, j),
+                                __shfl_sync(0xffffffffu, tok.dl, j));
+                if (j < n && there) {
+                    if constexpr (kEpi == kPartial) {
+                        float* a = e.part + (split * e.cols + col + j) * e.rows + row;
+                        *a = e.first ? x : x + *a;
+                    } else {
+                        e.out[(col + j) * e.ldo + row] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                    }
                 }
-                *reinterpret_cast<float4*>(a + j) = w;
             }
         }
     }
@@ -194,6 +273,7 @@ __device__ __forceinline__ void xent_columns(const XentEpilogue& e, float (&v)[3
 // How the work is cut: tiles of the product, K blocks per share of the sum, shares.
 struct XentPlan {
     int tm, tn, nkb, per_split, splits;
+    int bn, stages;  // columns of a tile (a multiple of 16; 256 where B is MN-major); stages of the ring
     int n_fastest;  // the order of the tiles: neighbours in the first index run at the same time
 };
 
@@ -201,23 +281,25 @@ struct XentPlan {
 // halves of A and B, reporting to the first CTA's barriers), warp 1 of the first CTA issues the
 // MMAs of both, warps 2-5 of each CTA take the accumulators of its 128 rows out of tensor
 // memory while the next tile's are being summed in the other 256 columns.
-template <int kEpi, bool AMN, bool BMN>
+template <int kEpi, bool AMN, bool BMN, bool kT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
 xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                  const XentPlan plan, const XentEpilogue e) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    XentBarriers& bar = *reinterpret_cast<XentBarriers*>(smem_raw + (base - raw) + kXStages * kXStageBytes);
+    XentBarriers& bar = *reinterpret_cast<XentBarriers*>(smem_raw + (base - raw) + kXStageSpace);
     volatile int* abort_flag = &bar.abort_flag;
     unsigned* status = &g_xent_status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int tiles = plan.tm * plan.tn, items = tiles * plan.splits;
+    const int stages = plan.stages, half_bn = plan.bn / 2;
+    const uint32_t stage_bytes = kXABytes + (uint32_t)half_bn * 128;
 
     if (threadIdx.x == 0) {
-        for (int st = 0; st < kXStages; ++st) {
+        for (int st = 0; st < stages; ++st) {
             mbar_init(smem_u32(&bar.full[st]), 1);
             mbar_init(smem_u32(&bar.empty[st]), 1);
         }
@@ -259,45 +341,49 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
     if (warp == 0) {
         if (lane == 0) {
             fence_proxy_async_global();  // dz was written by ordinary stores of the kernel before
-            int it = 0;  // K blocks so far
+            int it = 0, st = 0;  // K blocks so far, and the ring's stage and phase
+            uint32_t ph = 0;
             bool ok = true;
             for (int item = pair; item < items && ok; item += pairs) {
                 int tm, tn, kb0, kb1;
                 tile_of(item, tm, tn, kb0, kb1);
-                const int m0 = tm * kXTile + (int)rank * kXHalfTile, n0 = tn * kXTile + (int)rank * kXHalfTile;
+                const int m0 = tm * kXTile + (int)rank * kXHalfTile, n0 = tn * plan.bn + (int)rank * half_bn;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int st = it % kXStages;
-                    const uint32_t ph = (uint32_t)(it / kXStages) & 1u;
                     if (!mbar_wait(smem_u32(&bar.empty[st]), ph ^ 1u, abort_flag, status)) {
                         ok = false;
                         break;
                     }
                     const uint32_t full = in_leader(smem_u32(&bar.full[st]));
-                    if (rank == 0) mbar_expect_tx(smem_u32(&bar.full[st]), 2u * kXStageBytes);
-                    const uint32_t dst = base + (uint32_t)(st * kXStageBytes);
+                    if (rank == 0) mbar_expect_tx(smem_u32(&bar.full[st]), 2u * stage_bytes);
+                    const uint32_t dst = base + (uint32_t)st * stage_bytes;
                     if constexpr (AMN) {
                         pair_load_2d(dst, &amap, m0, kb * kXK, full);
-                        pair_load_2d(dst + kXHalf, &amap, m0 + 64, kb * kXK, full);
+                        pair_load_2d(dst + kXBox, &amap, m0 + 64, kb * kXK, full);
                     } else {
                         pair_load_2d(dst, &amap, kb * kXK, m0, full);
                     }
                     if constexpr (BMN) {
-                        pair_load_2d(dst + kXTileBytes, &bmap, n0, kb * kXK, full);
-                        pair_load_2d(dst + kXTileBytes + kXHalf, &bmap, n0 + 64, kb * kXK, full);
+                        pair_load_2d(dst + kXABytes, &bmap, n0, kb * kXK, full);
+                        pair_load_2d(dst + kXABytes + kXBox, &bmap, n0 + 64, kb * kXK, full);
                     } else {
-                        pair_load_2d(dst + kXTileBytes, &bmap, kb * kXK, n0, full);
+                        pair_load_2d(dst + kXABytes, &bmap, kb * kXK, n0, full);
+                    }
+                    if (++st == stages) {
+                        st = 0;
+                        ph ^= 1u;
                     }
                 }
             }
             // given up: what the pair has in flight reports to the first CTA's barriers
             if (!ok && rank == 0)
-                for (int i = it < kXStages ? 0 : it - kXStages; i < it; ++i)
-                    mbar_drain(smem_u32(&bar.full[i % kXStages]), (uint32_t)(i / kXStages) & 1u);
+                for (int i = it < stages ? 0 : it - stages; i < it; ++i)
+                    mbar_drain(smem_u32(&bar.full[i % stages]), (uint32_t)(i / stages) & 1u);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = xent_idesc(AMN, BMN);
-            int it = 0, n = 0;
+            const uint32_t idesc = xent_idesc(AMN, BMN, plan.bn);
+            int n = 0, st = 0;
+            uint32_t ph = 0;
             bool ok = true;
             for (int item = pair; item < items && ok; item += pairs, ++n) {
                 int tm, tn, kb0, kb1;
@@ -309,14 +395,13 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * kXTile);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int st = it % kXStages;
-                    if (!mbar_wait(smem_u32(&bar.full[st]), (uint32_t)(it / kXStages) & 1u, abort_flag, status)) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(smem_u32(&bar.full[st]), ph, abort_flag, status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t aaddr = base + (uint32_t)(st * kXStageBytes), baddr = aaddr + kXTileBytes;
+                    const uint32_t aaddr = base + (uint32_t)st * stage_bytes, baddr = aaddr + kXABytes;
                     const uint64_t ad = AMN ? xent_desc_mn(aaddr) : sw128_desc(aaddr);
                     const uint64_t bd = BMN ? xent_desc_mn(baddr) : sw128_desc(baddr);
                     constexpr uint64_t astep = AMN ? 2048 / 16 : 32 / 16, bstep = BMN ? 2048 / 16 : 32 / 16;
@@ -324,6 +409,10 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                     for (int k = 0; k < kXK / 16; ++k)
                         pair_mma(d, ad + (uint64_t)k * astep, bd + (uint64_t)k * bstep, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
                     pair_commit(smem_u32(&bar.empty[st]));
+                    if (++st == stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
                 if (ok) pair_commit(smem_u32(&bar.acc_full[acc]));
             }
@@ -341,34 +430,29 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
             const int split = tile_of(item, tm, tn, kb0, kb1);
             const int acc = n & 1;
             const int64_t row = (int64_t)tm * kXTile + (int)rank * kXHalfTile + quad * 32 + lane;
-            const bool there = row < e.rows;
-            int64_t label = -1;
-            float lse2 = 0.f, dl = 0.f;
-            if constexpr (kEpi == kStats || kEpi == kDz) {
-                label = there ? (int64_t)e.labels[row] : -1;
-                if (label >= e.vocab) label = -1;
-            }
-            if constexpr (kEpi == kDz) {
-                lse2 = there ? e.lse[row] * kLog2e : 0.f;
-                dl = there && label >= 0 ? e.dloss[row] : 0.f;
-            }
+            const int64_t slot = kT ? ((int64_t)tm * 2 + rank) * 4 + quad : tn;
+            XentToken tok = xent_token<kEpi>(e, row, !kT && row < e.rows);
             if (!mbar_wait(smem_u32(&bar.acc_full[acc]), (uint32_t)(n >> 1) & 1u, abort_flag, status)) break;
             tc_fence_after();
             float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-            for (int c0 = 0; c0 < kXTile; c0 += 32) {
+            for (int c0 = 0; c0 < plan.bn; c0 += 32) {
+                const int64_t col = (int64_t)tn * plan.bn + c0, left = e.cols - col;
+                const int room = plan.bn - c0 < 32 ? plan.bn - c0 : 32, here = left < room ? (int)left : room;
+                if (here <= 0) break;
+                if constexpr (kT) tok = xent_token<kEpi>(e, col + lane, lane < here);
                 uint32_t w[32];
                 tmem_ld32(tmem + lanes + (uint32_t)(acc * kXTile + c0), w);
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
-                xent_columns<kEpi>(e, v, row, there, (int64_t)tn * kXTile + c0, split, label, lse2, dl, m, s);
+                xent_columns<kEpi, kT>(e, v, row, col, here, split, slot, tok, m, s);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_at(in_leader(smem_u32(&bar.acc_empty[acc])));
-            if constexpr (kEpi == kStats) {
-                if (there) e.stats[(int64_t)tn * e.rows + row] = make_float2(m, s);
+            if constexpr (kEpi == kStats && !kT) {
+                if (row < e.rows) e.stats[slot * e.rows + row] = make_float2(m, s);
             }
         }
     }
@@ -400,36 +484,35 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__
     }
 }
 
-// A warp per token joins the tiles' (maximum, sum) pairs: lane l takes tiles l, l + 32, ... in
-// order, then the lanes join in a tree (a fixed order).
-__global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict__ stats, const float* __restrict__ picked,
-                                                        const int32_t* __restrict__ labels, int64_t tokens,
-                                                        int64_t vocab, int tiles, float* __restrict__ loss,
-                                                        float* __restrict__ lse) {
+// A CTA per token joins the (maximum, sum) pairs of its slots: thread i takes slots i, i + 128,
+// ... in order, then the threads join in a tree (a fixed order).
+constexpr int kXJoinThreads = 128;
+
+__device__ __forceinline__ float2 xent_join(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x), f = m == -INFINITY ? 0.f : m;
+    return make_float2(m, a.y * xent_ex2((a.x - f) * kLog2e) + b.y * xent_ex2((b.x - f) * kLog2e));
+}
+
+__global__ void __launch_bounds__(kXJoinThreads)
+xent_join_kernel(const float2* __restrict__ stats, const float* __restrict__ picked, const int32_t* __restrict__ labels,
+                 int64_t tokens, int64_t vocab, int slots, float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ float2 warps[kXJoinThreads / 32];
     pdl_wait();
-    const int64_t row = blockIdx.x * (int64_t)(blockDim.x / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= tokens) return;
-    float m = -INFINITY, s = 0.f;
-    for (int t = lane; t < tiles; t += 32) {
-        const float2 p = stats[(int64_t)t * tokens + row];
-        const float mm = fmaxf(m, p.x), f = mm == -INFINITY ? 0.f : mm;
-        s = s * xent_ex2((m - f) * kLog2e) + p.y * xent_ex2((p.x - f) * kLog2e);
-        m = mm;
-    }
+    const int64_t row = blockIdx.x;
+    float2 r = make_float2(-INFINITY, 0.f);
+    for (int t = threadIdx.x; t < slots; t += kXJoinThreads) r = xent_join(r, stats[(int64_t)t * tokens + row]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        const float mm = fmaxf(m, m2), f = mm == -INFINITY ? 0.f : mm;
-        s = s * xent_ex2((m - f) * kLog2e) + s2 * xent_ex2((m2 - f) * kLog2e);
-        m = mm;
-    }
-    if (lane == 0) {
-        const float logs = logf(s);
-        lse[row] = m + logs;
+    for (int o = 16; o > 0; o >>= 1)
+        r = xent_join(r, make_float2(__shfl_xor_sync(0xffffffffu, r.x, o), __shfl_xor_sync(0xffffffffu, r.y, o)));
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = r;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kXJoinThreads / 32; ++w) r = xent_join(r, warps[w]);
+        const float logs = logf(r.y);
+        lse[row] = r.x + logs;
         const int32_t label = labels[row];
         // (m - z) + log s: exact difference first
-        loss[row] = label >= 0 && label < vocab ? (m - picked[row]) + logs : 0.f;
+        loss[row] = label >= 0 && label < vocab ? (r.x - picked[row]) + logs : 0.f;
     }
 }
 
@@ -459,36 +542,44 @@ bool xent_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t cut(int64_t v, int64_t a) { return (v + a - 1) / a; }
 
-template <int kEpi, bool AMN, bool BMN>
-int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K,
+template <int kEpi, bool AMN, bool BMN, bool kT>
+int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K, int bn,
                 int splits, bool n_fastest, const XentEpilogue& e, cudaStream_t stream) {
     static unsigned long long init_mask = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NQ_ERR_CUDA;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(__atomic_load_n(&init_mask, __ATOMIC_ACQUIRE) & bit)) {
-        if (cudaFuncSetAttribute(xent_gemm_kernel<kEpi, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kXSmem) !=
+        if (cudaFuncSetAttribute(xent_gemm_kernel<kEpi, AMN, BMN, kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kXSmem) !=
             cudaSuccess)
             return NQ_ERR_CUDA;
         __atomic_fetch_or(&init_mask, bit, __ATOMIC_RELEASE);
     }
     CUtensorMap amap, bmap;
     if (!(AMN ? xent_map(&amap, A, K, M, lda, kXK) : xent_map(&amap, A, M, K, lda, kXHalfTile)) ||
-        !(BMN ? xent_map(&bmap, B, K, N, ldb, kXK) : xent_map(&bmap, B, N, K, ldb, kXHalfTile)))
+        !(BMN ? xent_map(&bmap, B, K, N, ldb, kXK) : xent_map(&bmap, B, N, K, ldb, bn / 2)))
         return NQ_ERR_CUDA;
     XentPlan plan;
     plan.tm = (int)cut(M, kXTile);
-    plan.tn = (int)cut(N, kXTile);
+    plan.tn = (int)cut(N, bn);
+    plan.bn = bn;
+    plan.stages = kXStageSpace / (kXABytes + 64 * bn);
+    if (plan.stages > kXMaxStages) plan.stages = kXMaxStages;
     plan.nkb = (int)cut(K, kXK);
     plan.per_split = (int)cut(plan.nkb, splits);
     plan.splits = splits;
     plan.n_fastest = n_fastest;
     const int64_t items = (int64_t)plan.tm * plan.tn * splits, pairs = sm_count() / 2;
-    return launch_pdl(xent_gemm_kernel<kEpi, AMN, BMN>, dim3((unsigned)(2 * (items < pairs ? items : pairs))),
+    return launch_pdl(xent_gemm_kernel<kEpi, AMN, BMN, kT>, dim3((unsigned)(2 * (items < pairs ? items : pairs))),
                       dim3(kXThreads), (size_t)kXSmem, stream, amap, bmap, plan, e) == cudaSuccess
                ? NQ_OK
                : NQ_ERR_CUDA;
 }
+
+// Up to this many tokens the products with W are transposed: W's rows (or columns) are the
+// tile's 256 rows, and all tokens fit its columns, of which only as many as needed are summed.
+constexpr int64_t kXFewTokens = 256;
+int few_columns(int64_t tokens) { return (int)round_up(tokens, 16); }
 
 // Classes per piece of the backward: as many whole column tiles as dz's scratch holds.
 int64_t piece_classes(int64_t tokens, int64_t vocab) {
@@ -502,10 +593,11 @@ int64_t piece_classes(int64_t tokens, int64_t vocab) {
 // shares' sums (4 bytes written and read again per element, about 1.2 MB in the time of a K
 // block) added; no share is empty and all fit their scratch.
 int dh_splits(int64_t tokens, int64_t classes, int64_t d) {
-    const int64_t tiles = cut(tokens, kXTile) * cut(d, kXTile), nkb = cut(classes, kXK), pairs = sm_count() / 2;
+    const int64_t tiles = (tokens <= kXFewTokens ? 1 : cut(tokens, kXTile)) * cut(d, kXTile), nkb = cut(classes, kXK);
+    const int64_t pairs = sm_count() / 2;
     int best = 1;
     int64_t least = INT64_MAX;
-    for (int64_t s = 1; s <= 16 && s <= nkb; ++s) {
+    for (int64_t s = 1; s <= 64 && s <= nkb; ++s) {
         if (s > 1 && 4 * s * tokens * d > kXSumBytes) break;
         const int64_t per = cut(nkb, s);
         if (cut(nkb, per) != s) continue;
@@ -531,10 +623,16 @@ BackwardPlan plan_backward(int64_t tokens, int64_t vocab, int64_t d) {
     return p;
 }
 
+// Pairs per token that the forward leaves to be joined: one per column tile, or one per warp
+// of the transposed product.
+int64_t stat_slots(int64_t tokens, int64_t vocab) {
+    return tokens <= kXFewTokens ? 8 * cut(vocab, kXTile) : cut(vocab, kXTile);
+}
+
 }  // namespace
 
 int64_t xent_fwd_scratch_bytes(int64_t tokens, int64_t vocab) {
-    return round_up(8 * tokens * cut(vocab, kXTile), 256) + round_up(4 * tokens, 256);
+    return round_up(8 * tokens * stat_slots(tokens, vocab), 256) + round_up(4 * tokens, 256);
 }
 
 int64_t xent_bwd_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d) {
@@ -542,20 +640,47 @@ int64_t xent_bwd_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d) {
     return round_up(2 * tokens * p.piece, 256) + (p.direct ? 0 : round_up(4 * p.splits * tokens * d, 256));
 }
 
+// z of tokens and classes (nv rows of W), its epilogue kEpi: stats or dz.
+template <int kEpi>
+static int xent_logits(const uint16_t* h, const uint16_t* W, int64_t tokens, int64_t nv, int64_t d, XentEpilogue e,
+                       cudaStream_t stream) {
+    if (tokens <= kXFewTokens) {
+        e.rows = nv;
+        e.cols = tokens;
+        return xent_launch<kEpi, false, false, true>(W, d, h, d, nv, tokens, d, few_columns(tokens), 1, false, e, stream);
+    }
+    e.rows = tokens;
+    e.cols = nv;
+    return xent_launch<kEpi, false, false, false>(h, d, W, d, tokens, nv, d, kXTile, 1, false, e, stream);
+}
+
+// dz W: shares of the sum over the classes, or the whole as bf16.
+template <int kEpi>
+static int xent_dh(const uint16_t* dz, int64_t piece, const uint16_t* W, int64_t tokens, int64_t nv, int64_t d, int splits,
+                   XentEpilogue e, cudaStream_t stream) {
+    if (tokens <= kXFewTokens) {
+        e.rows = d;
+        e.cols = tokens;
+        return xent_launch<kEpi, true, false, true>(W, d, dz, piece, d, tokens, nv, few_columns(tokens), splits, false, e,
+                                                    stream);
+    }
+    e.rows = tokens;
+    e.cols = d;
+    return xent_launch<kEpi, false, true, false>(dz, piece, W, d, tokens, d, nv, kXTile, splits, false, e, stream);
+}
+
 int xent_forward(const uint16_t* h, const uint16_t* W, const int32_t* labels, int64_t tokens, int64_t vocab, int64_t d,
                  float* loss, float* lse, void* scratch, cudaStream_t stream) {
-    const int64_t tiles = cut(vocab, kXTile);
+    const int64_t slots = stat_slots(tokens, vocab);
     XentEpilogue e = {};
-    e.rows = tokens;
-    e.cols = e.vocab = vocab;
+    e.vocab = vocab;
     e.labels = labels;
     e.stats = static_cast<float2*>(scratch);
-    e.picked = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(8 * tokens * tiles, 256));
-    const int rc = xent_launch<kStats, false, false>(h, d, W, d, tokens, vocab, d, 1, false, e, stream);
+    e.picked = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(8 * tokens * slots, 256));
+    const int rc = xent_logits<kStats>(h, W, tokens, vocab, d, e, stream);
     if (rc != NQ_OK) return rc;
-    return launch_pdl(xent_join_kernel, dim3((unsigned)((tokens + 7) / 8)), dim3(256), 0, stream,
-                      (const float2*)e.stats, (const float*)e.picked, labels, tokens, vocab, (int)tiles, loss, lse) ==
-                   cudaSuccess
+    return launch_pdl(xent_join_kernel, dim3((unsigned)tokens), dim3(kXJoinThreads), 0, stream, (const float2*)e.stats,
+                      (const float*)e.picked, labels, tokens, vocab, (int)slots, loss, lse) == cudaSuccess
                ? NQ_OK
                : NQ_ERR_CUDA;
 }
@@ -570,8 +695,6 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
     for (int64_t v0 = 0; v0 < vocab; v0 += piece) {
         const int64_t nv = vocab - v0 < piece ? vocab - v0 : piece;
         XentEpilogue e = {};
-        e.rows = tokens;
-        e.cols = nv;
         e.labels = labels;
         e.label0 = v0;
         e.vocab = vocab;
@@ -579,7 +702,7 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
         e.dloss = dloss;
         e.out = dz;
         e.ldo = piece;
-        int rc = xent_launch<kDz, false, false>(h, d, W + v0 * d, d, tokens, nv, d, 1, false, e, stream);
+        int rc = xent_logits<kDz>(h, W + v0 * d, tokens, nv, d, e, stream);
         if (rc != NQ_OK) return rc;
         if (dW) {
             XentEpilogue g = {};
@@ -587,24 +710,21 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
             g.cols = d;
             g.out = dW + v0 * d;
             g.ldo = d;
-            rc = xent_launch<kToBf16, true, true>(dz, piece, h, d, nv, d, tokens, 1, true, g, stream);
+            rc = xent_launch<kToBf16, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream);
             if (rc != NQ_OK) return rc;
         }
         if (dh) {
             XentEpilogue g = {};
-            g.rows = tokens;
-            g.cols = d;
             if (plan.direct) {
                 g.out = dh;
                 g.ldo = d;
-                rc = xent_launch<kToBf16, false, true>(dz, piece, W + v0 * d, d, tokens, d, nv, 1, false, g, stream);
+                rc = xent_dh<kToBf16>(dz, piece, W + v0 * d, tokens, nv, d, 1, g, stream);
             } else {
                 // the last piece may have fewer K blocks than shares: then it adds to the first ones
                 g.part = part;
                 g.first = v0 == 0;
                 const int64_t nkb = cut(nv, kXK), per = cut(nkb, plan.splits);
-                rc = xent_launch<kPartial, false, true>(dz, piece, W + v0 * d, d, tokens, d, nv, (int)cut(nkb, per), false,
-                                                        g, stream);
+                rc = xent_dh<kPartial>(dz, piece, W + v0 * d, tokens, nv, d, (int)cut(nkb, per), g, stream);
             }
             if (rc != NQ_OK) return rc;
         }

@@ -380,8 +380,9 @@ int nq_pack_q4(const uint8_t* codes, int64_t rows, int64_t cols, uint32_t* out, 
  *            m, n at most 1<<20
  *   batch  : 0 (a no-op) to 524280 (else NQ_ERR_BATCH).  Made for the few tokens of a decode
  *            step: up to 8 tokens read the codes once, more read them again for every 8.
- * Products are exact and sums are fp32: |error| <= (48 + n/256) 2^-23 sum_j |s| (|c - 8| +
- * |z - 8|) |x_j|.  Each token's result does not depend on the others.
+ * Products are exact and sums are fp32: |error| <= (48 + n/32) 2^-23 sum_j |s| (c + |z|) |x_j|.
+ * Each token's result does not depend on the others; an infinity or a NaN in a token's x makes
+ * that token's results NaN or infinite.
  */
 int nq_q4_linear_fwd(const void* x, const uint32_t* Wq, const void* scales, const void* zeros, int64_t m, int64_t n,
                      int64_t group, int64_t batch, float* y, void* stream);
@@ -442,8 +443,8 @@ int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const i
  * of the tensor cores beside h and W), sums over classes and tokens are fp32, results are
  * rounded once to bfloat16: |error of dh_ij| <= 2^-8 (sum_v |dz_iv W_vj| + |dh_ij|), likewise
  * dW.  The scratch of bwd is bounded: dz exists for a piece of the vocabulary at a time (at
- * most 256 MB, or 128 classes), plus 4 tokens d bytes of sums when there is more than one
- * piece.  Repeated calls agree bit for bit.  A bounded device wait that gave up is reported by
+ * most 256 MB, or 256 classes), and dh's sums in fp32 in shares (at most 256 MB, or 4 tokens d
+ * bytes).  Repeated calls agree bit for bit.  A bounded device wait that gave up is reported by
  * nq_device_status.
  */
 int64_t nq_linear_cross_entropy_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d, int backward);

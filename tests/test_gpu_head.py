@@ -3,9 +3,9 @@ products with 4-bit weights, the distillation loss against a teacher's top logit
 gradient, and the cross entropy of a dense head with its gradients.
 
 Tolerances.  u = 2^-23 (a truncated fp32 step; a rounded one is half of it).
-  * 4-bit products: exact products; 24 accumulator steps within a group, 2 to apply scale and
-    zero point, n / 256 group sums per warp at most, 8 warps: (48 + n / 256) u of the sum of
-    the terms' magnitudes.
+  * 4-bit products: exact products c x; 24 accumulator steps within a group (the sum of x takes
+    fewer), 3 to apply zero point and scale, at most n / 32 groups and 16 warps to add: with
+    sums of c x and of z x taken apart, (48 + n / 32) u of sum |s| (c + |z|) |x| bounds them.
   * distillation: a thread adds V / 512 exponentials one after another, 9 tree steps and a few
     joins follow; an exponential is off by 2 u and by its argument's rounding (|argument| u,
     arguments up to 40 where it matters): the relative error of a sum is below
@@ -62,8 +62,8 @@ def q4_check(y, codes, scales, z, x, n, group):
     zz = z.double().repeat_interleave(group, 1) if z is not None else torch.full_like(c, 8.0)
     s = scales.double().repeat_interleave(group, 1)
     ref = x.double() @ ((c - zz) * s).T
-    mag = x.double().abs() @ (((c - 8).abs() + (zz - 8).abs()) * s.abs()).T
-    assert torch.all((y.double() - ref).abs() <= (48 + n / 256) * U * mag)
+    mag = x.double().abs() @ ((c + zz.abs()) * s.abs()).T
+    assert torch.all((y.double() - ref).abs() <= (48 + n / 32) * U * mag)
 
 
 Q4_SHAPES = [
@@ -71,6 +71,8 @@ Q4_SHAPES = [
     (15, 384, 128, 3, False), (513, 384, 32, 9, True), (512, 512, 128, 1, False), (33, 640, 64, 17, False),
     (100, 8192, 32, 3, True), (2049, 1152, 32, 1, True), (4096, 4096, 128, 8, False), (32001, 512, 64, 2, True),
     (28672, 1024, 128, 5, True), (260, 2176, 128, 16, True),
+    (301, 1408, 128, 4, True), (77, 11008, 128, 2, True), (53, 2176, 64, 3, False), (95, 2176, 32, 1, True),
+    (300, 8320, 32, 8, True), (3000, 28672, 64, 8, True), (70, 28672, 32, 3, False), (5000, 66048, 128, 1, True),
 ]
 
 
