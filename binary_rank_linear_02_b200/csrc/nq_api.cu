@@ -829,8 +829,8 @@ int nq_device_status(void* stream) {
     unsigned word = 0;
     if (cudaMemcpy(&word, ws->status + 1, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess) return NQ_ERR_CUDA;
     if (word != 0 && cudaMemset(ws->status + 1, 0, sizeof(unsigned)) != cudaSuccess) return NQ_ERR_CUDA;
-    // the 4-bit products and the cross entropy have words of their own
-    for (auto take : {q4_take_status, xent_take_status}) {
+    // the kernels of the output head have words of their own
+    for (auto take : {q4_take_status, distill_take_status, xent_take_status}) {
         unsigned head = 0;
         if (take(&head) != NQ_OK) return NQ_ERR_CUDA;
         if (word == 0) word = head;

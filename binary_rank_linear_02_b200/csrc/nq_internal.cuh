@@ -179,6 +179,7 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
                   cudaStream_t stream);
 // read and clear the status words of these kernels (the device is idle)
 int q4_take_status(unsigned* word);
+int distill_take_status(unsigned* word);
 int xent_take_status(unsigned* word);
 
 }  // namespace nq

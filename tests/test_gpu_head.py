@@ -207,7 +207,8 @@ DISTILL = [
     (1, 1, 1, 1, False, 1.0), (2, 7, 7, 3, True, 2.0), (3, 8, 16, 8, True, 1.0), (3, 9, 9, 1, False, 4.0),
     (5, 100, 101, 20, True, 0.5), (4, 1001, 1001, 64, False, 1.0), (7, 4099, 4224, 50, True, 2.0),
     (5, 32000, 32000, 256, True, 1.0), (4, 50257, 50304, 33, False, 2.0), (3, 128001, 128001, 1024, True, 1.5),
-    (2, 262144, 262144, 8, True, 1.0), (300, 515, 515, 5, True, 1.0),
+    (2, 262144, 262144, 8, True, 1.0), (300, 515, 515, 5, True, 1.0), (2, 1 << 20, 1 << 20, 9, True, 1.0),
+    (200, 20003, 20003, 7, False, 1.0), (160, 70001, 70001, 11, True, 2.0),
 ]
 
 
