@@ -942,11 +942,25 @@ int nq_lowrank_linear_fwd(const void* x, const uint32_t* Upk, const uint32_t* Vp
 // ---------------------------------------------------------------- the output head
 
 // The head's entry points take device pointers alone, 16-byte aligned; null ones are optional.
+// (One query of the current device for all: these calls cost about as much as they compute.)
 static int check_device_pointers(const void* const* ptrs, int count) {
     for (int i = 0; i < count; ++i)
         if (ptrs[i] && !aligned16(ptrs[i])) return NQ_ERR_ALIGN;
-    for (int i = 0; i < count; ++i)
-        if (ptrs[i] && pointer_kind(ptrs[i]) != kDeviceMem) return NQ_ERR_PTRKIND;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return NQ_ERR_PTRKIND;
+    }
+    for (int i = 0; i < count; ++i) {
+        if (!ptrs[i]) continue;
+        cudaPointerAttributes attr;
+        if (cudaPointerGetAttributes(&attr, ptrs[i]) != cudaSuccess) {
+            cudaGetLastError();
+            return NQ_ERR_PTRKIND;
+        }
+        if (attr.type != cudaMemoryTypeManaged && (attr.type != cudaMemoryTypeDevice || attr.device != dev))
+            return NQ_ERR_PTRKIND;
+    }
     return NQ_OK;
 }
 

@@ -14,6 +14,7 @@ tensor-level conveniences ``pack_signs``, ``unpack_signs``, ``lowrank_linear_fwd
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -237,7 +238,8 @@ def _stream(stream, *tensors) -> int:
 
     for t in tensors:
         if isinstance(t, torch.Tensor) and t.is_cuda:
-            return torch.cuda.current_stream(t.device).cuda_stream
+            # the handle alone: building the stream object around it costs over 2 us a call
+            return torch._C._cuda_getCurrentRawStream(t.get_device())
     return 0
 
 
@@ -494,15 +496,26 @@ def bits_per_weight_envelope(m: int, n: int, r: int, l: int) -> float:
 
 # ------------------------------------------------------------------ the output head
 
-def _typed(t, name: str, *dtypes) -> None:
-    """The head's calls pass pointers of typed buffers on: a wrong element type is refused here."""
-    if t is not None and t.dtype not in dtypes:
+# The head's calls are made once per token or step and cost the host about as much as the GPU:
+# each argument is looked at once (element type, shape, contiguity; anything else is the
+# library's to check), and scratch sizes are remembered by the sizes they belong to.
+
+def _arg(t, name: str, dtypes, shape) -> int:
+    """The address of a contiguous tensor of one of these element types and this shape."""
+    if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype}, want {' or '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
+    assert t.is_contiguous(), "tensor must be contiguous"
+    return t.data_ptr()
 
 
-def _shaped(t, name: str, *shape) -> None:
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, want {shape}")
+@functools.lru_cache(maxsize=None)
+def _head_types():
+    import torch
+
+    return {"bf16": (torch.bfloat16, torch.int16), "fp16": (torch.float16, torch.int16), "words": (torch.int32, torch.uint32),
+            "f32": (torch.float32,), "i32": (torch.int32,), "logits": (torch.float32, torch.bfloat16)}
 
 
 def pack_q4(codes, out=None, stream=None):
@@ -517,7 +530,7 @@ def pack_q4(codes, out=None, stream=None):
     else:
         import torch
 
-        _typed(codes, "codes", torch.uint8)
+        _arg(codes, "codes", (torch.uint8,), (rows, cols))
         if out is None:
             out = torch.empty((rows, wpr), dtype=torch.int32, device=codes.device)
     _check(_lib.nq_pack_q4(_ptr(codes), rows, cols, _ptr(out), _stream(stream, codes)), "nq_pack_q4")
@@ -530,49 +543,34 @@ def q4_linear_fwd(x, Wq, scales, m: int, n: int, group: int, zeros=None, y=None,
     x: batch x n (or n) bfloat16; Wq: m x n/8 words of pack_q4; scales and zeros: m x n/group
     fp16 (zeros None: 8 everywhere); bfloat16 and fp16 may be given as int16 bit patterns.
     """
-    import torch
-
+    types = _head_types()
     batch = x.shape[0] if x.dim() == 2 else 1
-    _typed(x, "x", torch.bfloat16, torch.int16)
-    _typed(Wq, "Wq", torch.int32, torch.uint32)
-    _typed(scales, "scales", torch.float16, torch.int16)
-    _typed(zeros, "zeros", torch.float16, torch.int16)
-    _shaped(x, "x", *((batch, n) if x.dim() == 2 else (n,)))
-    _shaped(Wq, "Wq", m, n // 8)
-    if group in (32, 64, 128):  # any other group is the library's to refuse
-        _shaped(scales, "scales", m, n // group)
-        _shaped(zeros, "zeros", m, n // group)
+    xp = _arg(x, "x", types["bf16"], (batch, n) if x.dim() == 2 else (n,))
+    wp = _arg(Wq, "Wq", types["words"], (m, n // 8))
+    groups = (m, n // group) if group in (32, 64, 128) else scales.shape  # any other group is the library's to refuse
+    sp = _arg(scales, "scales", types["fp16"], groups)
+    zp = 0 if zeros is None else _arg(zeros, "zeros", types["fp16"], groups)
     if y is None:
-        y = torch.empty((batch, m), dtype=torch.float32, device=x.device)
-    _typed(y, "y", torch.float32)
-    _check(_lib.nq_q4_linear_fwd(_ptr(x), _ptr(Wq), _ptr(scales), _ptr(zeros), m, n, group, batch, _ptr(y),
-                                 _stream(stream, x)), "nq_q4_linear_fwd")
+        y = x.new_empty((batch, m), dtype=types["f32"][0])
+        yp = y.data_ptr()
+    else:
+        yp = _arg(y, "y", types["f32"], (batch, m))
+    status = _lib.nq_q4_linear_fwd(xp, wp, sp, zp, m, n, group, batch, yp, _stream(stream, x))
+    if status:
+        _check(status, "nq_q4_linear_fwd")
     return y
 
 
-def _logit_type(dtype) -> int:
-    import torch
-
-    if dtype == torch.float32:
-        return NQ_F32
-    if dtype == torch.bfloat16:
-        return NQ_BF16
-    raise TypeError(f"logits: {dtype}, want torch.float32 or torch.bfloat16")
-
-
-def _distill_args(logits, ids, teacher, vocab, teacher_lse, dloss=None):
-    import torch
-
+def _distill_args(logits, ids, teacher, teacher_lse, dloss):
+    """(tokens, ld, k, logits' type, addresses of ids, teacher, teacher_lse, dloss, logits)"""
+    types = _head_types()
     tokens, ld = logits.shape
     k = ids.shape[1]
-    _typed(ids, "ids", torch.int32)
-    for t, name in ((teacher, "teacher"), (teacher_lse, "teacher_lse"), (dloss, "dloss")):
-        _typed(t, name, torch.float32)
-    _shaped(ids, "ids", tokens, k)
-    _shaped(teacher, "teacher", tokens, k)
-    _shaped(teacher_lse, "teacher_lse", tokens)
-    _shaped(dloss, "dloss", tokens)
-    return tokens, ld, k, _logit_type(logits.dtype)
+    zp = _arg(logits, "logits", types["logits"], (tokens, ld))
+    return (tokens, ld, k, NQ_F32 if logits.dtype == types["logits"][0] else NQ_BF16, zp,
+            _arg(ids, "ids", types["i32"], (tokens, k)), _arg(teacher, "teacher", types["f32"], (tokens, k)),
+            0 if teacher_lse is None else _arg(teacher_lse, "teacher_lse", types["f32"], (tokens,)),
+            0 if dloss is None else _arg(dloss, "dloss", types["f32"], (tokens,)))
 
 
 def distill_topk_fwd(logits, ids, teacher, vocab: int, temperature: float = 1.0, teacher_lse=None, loss=None,
@@ -581,13 +579,15 @@ def distill_topk_fwd(logits, ids, teacher, vocab: int, temperature: float = 1.0,
     first `vocab` columns) against the teacher's entries: ids (tokens x k int32, -1: absent) and
     their logits `teacher` (tokens x k float32); teacher_lse (tokens float32): log sum exp of the
     teacher's logits / temperature over its whole vocabulary, None: the teacher restricted to its list."""
-    import torch
-
-    tokens, ld, k, kind = _distill_args(logits, ids, teacher, vocab, teacher_lse)
+    tokens, ld, k, kind, zp, ip, up, lp, _ = _distill_args(logits, ids, teacher, teacher_lse, None)
     if loss is None:
-        loss = torch.empty((tokens,), dtype=torch.float32, device=logits.device)
-    _check(_lib.nq_distill_topk_fwd(_ptr(logits), kind, ld, _ptr(ids), _ptr(teacher), _ptr(teacher_lse), tokens, vocab,
-                                    k, temperature, _ptr(loss), _stream(stream, logits)), "nq_distill_topk_fwd")
+        loss = teacher.new_empty((tokens,))
+        op = loss.data_ptr()
+    else:
+        op = _arg(loss, "loss", _head_types()["f32"], (tokens,))
+    status = _lib.nq_distill_topk_fwd(zp, kind, ld, ip, up, lp, tokens, vocab, k, temperature, op, _stream(stream, logits))
+    if status:
+        _check(status, "nq_distill_topk_fwd")
     return loss
 
 
@@ -596,71 +596,87 @@ def distill_topk_bwd(logits, ids, teacher, vocab: int, dloss, temperature: float
     """(dlogits, loss): the gradient of sum_i dloss[i] loss[i] with respect to the logits
     (tokens x ld, torch.bfloat16 unless `dtype` says torch.float32; columns from `vocab` on are
     zero) and the losses, from one read of the logits.  Arguments as distill_topk_fwd."""
-    import torch
-
-    tokens, ld, k, kind = _distill_args(logits, ids, teacher, vocab, teacher_lse, dloss)
+    types = _head_types()
+    tokens, ld, k, kind, zp, ip, up, lp, wp = _distill_args(logits, ids, teacher, teacher_lse, dloss)
     if dlogits is None:
-        dlogits = torch.empty((tokens, ld), dtype=dtype or torch.bfloat16, device=logits.device)
-    _shaped(dlogits, "dlogits", tokens, ld)
+        dlogits = logits.new_empty((tokens, ld), dtype=types["logits"][1] if dtype is None else dtype)
+    gp = _arg(dlogits, "dlogits", types["logits"], (tokens, ld))
     if loss is None:
-        loss = torch.empty((tokens,), dtype=torch.float32, device=logits.device)
-    _check(_lib.nq_distill_topk_bwd(_ptr(logits), kind, ld, _ptr(ids), _ptr(teacher), _ptr(teacher_lse), _ptr(dloss),
-                                    tokens, vocab, k, temperature, _ptr(loss), _ptr(dlogits),
-                                    _logit_type(dlogits.dtype), _stream(stream, logits)), "nq_distill_topk_bwd")
+        loss = teacher.new_empty((tokens,))
+        op = loss.data_ptr()
+    else:
+        op = _arg(loss, "loss", types["f32"], (tokens,))
+    status = _lib.nq_distill_topk_bwd(zp, kind, ld, ip, up, lp, wp, tokens, vocab, k, temperature, op, gp,
+                                      NQ_F32 if dlogits.dtype == types["logits"][0] else NQ_BF16, _stream(stream, logits))
+    if status:
+        _check(status, "nq_distill_topk_bwd")
     return dlogits, loss
 
 
 def _xent_args(h, W, labels):
-    import torch
-
+    types = _head_types()
     tokens, d = h.shape
     vocab = W.shape[0]
-    _typed(h, "h", torch.bfloat16, torch.int16)
-    _typed(W, "W", torch.bfloat16, torch.int16)
-    _typed(labels, "labels", torch.int32)
-    _shaped(W, "W", vocab, d)
-    _shaped(labels, "labels", tokens)
-    return tokens, vocab, d
+    return (tokens, vocab, d, _arg(h, "h", types["bf16"], (tokens, d)), _arg(W, "W", types["bf16"], (vocab, d)),
+            _arg(labels, "labels", types["i32"], (tokens,)))
 
 
-def _xent_scratch(tokens: int, vocab: int, d: int, backward: bool, device):
+@functools.lru_cache(maxsize=1024)
+def _xent_scratch_bytes(tokens: int, vocab: int, d: int, backward: int, device: int) -> int:
+    # (by device: the plan goes by its number of SMs; sizes out of range, -1, are the call's to refuse)
+    return _lib.nq_linear_cross_entropy_scratch_bytes(tokens, vocab, d, backward)
+
+
+def _xent_scratch(h, tokens: int, vocab: int, d: int, backward: int):
+    """(scratch tensor, its size): the caching allocator's memory, so that calls on other streams
+    and captured graphs have their own."""
+    size = max(_xent_scratch_bytes(tokens, vocab, d, backward, h.get_device()), 16)
+    return h.new_empty((size,), dtype=_scratch_type()), size
+
+
+@functools.lru_cache(maxsize=None)
+def _scratch_type():
     import torch
 
-    size = _lib.nq_linear_cross_entropy_scratch_bytes(tokens, vocab, d, int(backward))
-    # at least a byte, so that the pointer is one; sizes out of range are the call's to refuse
-    return torch.empty((max(size, 16),), dtype=torch.uint8, device=device), size
+    return torch.uint8
 
 
 def linear_cross_entropy_fwd(h, W, labels, loss=None, lse=None, stream=None):
     """(loss, lse), float32 per token: cross entropy of softmax(h W^T) against int32 labels (a
     label outside the vocabulary does not count: loss 0), without the logits in memory.
     h: tokens x d, W: vocab x d, bfloat16."""
-    import torch
-
-    tokens, vocab, d = _xent_args(h, W, labels)
-    loss = torch.empty((tokens,), dtype=torch.float32, device=h.device) if loss is None else loss
-    lse = torch.empty((tokens,), dtype=torch.float32, device=h.device) if lse is None else lse
-    _typed(loss, "loss", torch.float32)
-    _typed(lse, "lse", torch.float32)
-    scratch, size = _xent_scratch(tokens, vocab, d, False, h.device)
-    _check(_lib.nq_linear_cross_entropy_fwd(_ptr(h), _ptr(W), _ptr(labels), tokens, vocab, d, _ptr(loss), _ptr(lse),
-                                            _ptr(scratch), size, _stream(stream, h)), "nq_linear_cross_entropy_fwd")
+    f32 = _head_types()["f32"]
+    tokens, vocab, d, hp, wp, lp = _xent_args(h, W, labels)
+    if loss is None:
+        loss = h.new_empty((tokens,), dtype=f32[0])
+        op = loss.data_ptr()
+    else:
+        op = _arg(loss, "loss", f32, (tokens,))
+    if lse is None:
+        lse = h.new_empty((tokens,), dtype=f32[0])
+        ep = lse.data_ptr()
+    else:
+        ep = _arg(lse, "lse", f32, (tokens,))
+    scratch, size = _xent_scratch(h, tokens, vocab, d, 0)
+    status = _lib.nq_linear_cross_entropy_fwd(hp, wp, lp, tokens, vocab, d, op, ep, scratch.data_ptr(), size,
+                                              _stream(stream, h))
+    if status:
+        _check(status, "nq_linear_cross_entropy_fwd")
     return loss, lse
 
 
 def linear_cross_entropy_bwd(h, W, labels, lse, dloss, need_dh: bool = True, need_dW: bool = True, stream=None):
     """(dh (tokens x d), dW (vocab x d)) bfloat16, None for one that is not needed: the gradients
     of sum_i dloss[i] loss[i], from the lse that linear_cross_entropy_fwd gave."""
-    import torch
-
-    tokens, vocab, d = _xent_args(h, W, labels)
-    for t, name in ((lse, "lse"), (dloss, "dloss")):
-        _typed(t, name, torch.float32)
-        _shaped(t, name, tokens)
-    dh = torch.empty((tokens, d), dtype=torch.bfloat16, device=h.device) if need_dh else None
-    dW = torch.empty((vocab, d), dtype=torch.bfloat16, device=h.device) if need_dW else None
-    scratch, size = _xent_scratch(tokens, vocab, d, True, h.device)
-    _check(_lib.nq_linear_cross_entropy_bwd(_ptr(h), _ptr(W), _ptr(labels), _ptr(lse), _ptr(dloss), tokens, vocab, d,
-                                            _ptr(dh), _ptr(dW), _ptr(scratch), size, _stream(stream, h)),
-           "nq_linear_cross_entropy_bwd")
+    types = _head_types()
+    tokens, vocab, d, hp, wp, lp = _xent_args(h, W, labels)
+    bf16 = types["bf16"][0]
+    ep, gp = _arg(lse, "lse", types["f32"], (tokens,)), _arg(dloss, "dloss", types["f32"], (tokens,))
+    dh = h.new_empty((tokens, d), dtype=bf16) if need_dh else None
+    dW = h.new_empty((vocab, d), dtype=bf16) if need_dW else None
+    scratch, size = _xent_scratch(h, tokens, vocab, d, 1)
+    status = _lib.nq_linear_cross_entropy_bwd(hp, wp, lp, ep, gp, tokens, vocab, d, dh.data_ptr() if need_dh else 0,
+                                              dW.data_ptr() if need_dW else 0, scratch.data_ptr(), size, _stream(stream, h))
+    if status:
+        _check(status, "nq_linear_cross_entropy_bwd")
     return dh, dW
