@@ -50,8 +50,9 @@ constexpr int kQCols = 128;                      // columns of a warp's block of
 constexpr int kQBlockBytes = 16 * kQCols / 2;    // 16 rows x 64 bytes
 constexpr int kQStageCols = kQWarps * kQCols;
 constexpr int kQCodeBytes = kQWarps * kQBlockBytes;
-constexpr int kQMaxStages = 8, kQMinStages = 3;
+constexpr int kQMaxStages = 8, kQMinStages = 4;  // an even number: a place of the ring is always the same team's
 constexpr int kQParts = 3;                       // sets whose shares wait to be added
+constexpr int kQTeam = kQWarps / 2;              // warps that share a stage, two blocks each
 constexpr int kQAdders = 4;                      // warps that add a set's shares
 constexpr int kQTokens = 8;                      // tokens per CTA (the n of the MMA)
 constexpr int kQSpace = 201 * 1024;              // dynamic shared memory, at most
@@ -179,7 +180,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(smem_u32(&full[i]), 33);  // the codes' bytes, and the fetching lanes' copies of scales
-            mbar_init(smem_u32(&empty[i]), kQWarps);
+            mbar_init(smem_u32(&empty[i]), kQTeam);
         }
         for (int i = 0; i < kQParts; ++i) {
             mbar_init(smem_u32(&written[i]), kQWarps);
@@ -212,7 +213,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
     if (warp == kQWarps) {
         // A lane's copies of a whole stage's scales: from where in the rows, to where.
         constexpr int kCopies = 8;
-        const int row_bytes = 2 * ngroups, stage_groups = p.blocks * kPerBlock, width = p.scale_copy;
+        const int row_bytes = 2 * ngroups, stage_groups = (p.blocks < blocks_all ? p.blocks : blocks_all) * kPerBlock, width = p.scale_copy;
         const int per_row = width == 2 ? 1 : 2 * stage_groups / width, copies = set_rows * per_row;
         int from[kCopies], to[kCopies];
 #pragma unroll
@@ -275,10 +276,12 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
         return;
     }
 
-    // The warp's block of a stage: block `block` of tile `sub` of the set.
+    // Two teams take the stages in turn.  The warp's two blocks of a stage (neighbours; one barrier
+    // and one set of addresses for both): blocks `block` and the next of tile `sub` of the set.
     const int g = lane >> 2, t = lane & 3;
-    const int sub = p.tps == 1 ? 0 : warp / p.blocks, block = p.tps == 1 ? warp : warp % p.blocks;
-    const bool placed = sub < p.tps;
+    const int team = warp / kQTeam, slot = 2 * (warp % kQTeam);
+    const int sub = p.tps == 1 ? 0 : slot / p.blocks, block = p.tps == 1 ? slot : slot % p.blocks;
+    const bool placed = sub < p.tps && block < p.blocks;
     const uint32_t frag = base + (uint32_t)(block * p.tps * kQBlockBytes + sub * kQBlockBytes + g * 64 +
                                             ((g >> 1 & 3) << 4) + 4 * t);  // piece j: XOR j << 4
     // (rows of an odd number of scales are copied from the 4-byte boundary before an odd one)
@@ -301,7 +304,8 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
 #pragma unroll
                 for (int w = 0; w < kQWarps; ++w) sum += part[buf][w][r][b];
             } else {
-                for (int w = 0; w < p.blocks; ++w) sum += part[buf][tile * p.blocks + w][r][b];
+                for (int w = 0; w < p.blocks / 2; ++w)
+                    sum += part[buf][tile * p.blocks / 2 + w][r][b] + part[buf][kQTeam + tile * p.blocks / 2 + w][r][b];
             }
             if (panels > 1) {  // (then a set is one tile)
                 float* kp = kept + set * (16 * kQTokens) + e;
@@ -315,7 +319,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
         if (lane == 0) mbar_arrive(smem_u32(&added[buf]));
     };
 
-    int st = 0, no = 0;
+    int st = team, no = 0, first = team;  // the team's next stage, and which of the next set's that is
     uint32_t phase = 0;
     for (int panel = 0; panel < panels; ++panel) {
         const int64_t pcol = (int64_t)panel * p.panel;
@@ -374,20 +378,26 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
 
         for (int set = 0; set < sets; ++set) {
             float out[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int k = 0; k < per_set; ++k) {
+            int k = first;
+            for (; k < per_set; k += 2) {
                 // (a wait that gives up is recorded and ends the others: the CTA runs out in bounded time)
                 mbar_wait(smem_u32(&full[st]), phase, abort_flag, &g_q4_status);
                 const int at_block = k * p.blocks + block;
-                if (placed && at_block < nblocks) {
-                    const uint32_t at = frag + (uint32_t)(st * kQCodeBytes), h_at = scale_at + (uint32_t)st * scale_stage;
+                const uint32_t at0 = frag + (uint32_t)(st * kQCodeBytes), h_at0 = scale_at + (uint32_t)st * scale_stage;
+                const unsigned char* xat0 = xrow + 2 * kQCols * at_block;
+                const float4* sat0 = srow + kPerBlock * pairs * at_block;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!placed || at_block + i >= nblocks) break;
+                    const uint32_t at = at0 + (uint32_t)(i * p.tps * kQBlockBytes), h_at = h_at0 + 2 * kPerBlock * i;
                     const uint2 ha = lds_halves<kPerBlock>(h_at), hb = lds_halves<kPerBlock>(h_at + scale_down);
                     uint2 za = ha, zb = hb;
                     if constexpr (kZeros) {
                         za = lds_halves<kPerBlock>(h_at + scale_bytes);
                         zb = lds_halves<kPerBlock>(h_at + scale_bytes + scale_down);
                     }
-                    const unsigned char* xat = xrow + 2 * kQCols * at_block;
-                    const float4* sat = srow + kPerBlock * pairs * at_block;
+                    const unsigned char* xat = xat0 + 2 * kQCols * i;
+                    const float4* sat = sat0 + kPerBlock * pairs * i;
                     float acc[4];
 #pragma unroll
                     for (int j = 0; j < kQCols / 32; ++j) {
@@ -423,13 +433,15 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
                         }
                     }
                 }
-                __syncwarp();  // the block was read by all lanes
+                __syncwarp();  // the blocks were read by all lanes
                 if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
-                if (++st == p.stages) {
-                    st = 0;
+                st += 2;
+                if (st >= p.stages) {
+                    st -= p.stages;
                     phase ^= 1u;
                 }
             }
+            first = k - per_set;
             // the warps' shares of the set's tiles
             if (no >= kQParts) mbar_wait(smem_u32(&added[no % kQParts]), (uint32_t)(no / kQParts - 1) & 1u, abort_flag, &g_q4_status);
             float(&mine)[16][kQTokens] = part[no % kQParts][warp];
@@ -506,7 +518,7 @@ int q4_launch(Q4Args p, const uint32_t* W, cudaStream_t stream) {
                (panels ? kQPanelSets * 16 * kQTokens * 4 : 0);
     };
     const int64_t row_blocks = p.n / kQCols;
-    p.blocks = (int)(row_blocks < kQWarps ? row_blocks : kQWarps);
+    p.blocks = (int)(row_blocks < kQWarps ? (row_blocks + 1) / 2 * 2 : kQWarps);
     const int64_t tiles = (p.m + 15) / 16;
     const int64_t token_groups = (p.batch + kQTokens - 1) / kQTokens;
     const int64_t at_once = sm_count() / token_groups > 0 ? sm_count() / token_groups : 1;
@@ -526,7 +538,7 @@ int q4_launch(Q4Args p, const uint32_t* W, cudaStream_t stream) {
         for (panel = p.n / kQStageCols * kQStageCols; panel > kQStageCols && bytes(panel, true) > room;) panel -= kQStageCols;
     p.panel = (int)panel;
     const int64_t fixed = bytes(panel, panels), fit = (kQSpace - fixed) / stage;
-    p.stages = (int)(fit < kQMaxStages ? fit : kQMaxStages);
+    p.stages = (int)(fit < kQMaxStages ? fit / 2 * 2 : kQMaxStages);
     const int64_t sets = (tiles + tps - 1) / tps;
     // the sets evenly over the CTAs that fit at a time
     int64_t per_cta = (sets + at_once - 1) / at_once;
