@@ -9,22 +9,29 @@
 //     dz_v  = dloss T (p_v tot - sum_{k: id_k = v} q_k - [v not listed] q_rest p_v / p_rest),
 // p_rest = the sum of p over the ids outside the list and tot = sum_k q_k + q_rest.
 //
-// One CTA per SM goes from token to token, with every step of a token hidden behind another's.
-// One warp streams the rows through a ring of 32 KB pieces in shared memory, by bulk copies (loads
-// into registers did not get past 4 TB/s, whatever was in flight); sixteen go through the pieces;
-// one works for them.  In the first pass over a row the sixteen keep a running maximum and sum per
-// thread (fp32) over the classes outside the list where the list matters (bits in shared memory
-// mark it), so p_rest is a sum of its own and never a difference.  Then comes the first pass of the
-// next row, and only then the second of this one, which writes the gradient as one exponential times
-// one factor per class.  It takes the row from L2 again: two rows per SM are what has to stay there
-// (with three CTAs per SM that each finish a row before the next it was read from HBM twice; with a
-// cluster that keeps it in shared memory the reductions, 20 us of a share's life, left HBM idle).
+// Two or three CTAs per SM go from token to token, with the steps of a token hidden behind
+// another's.  One warp streams the rows through a ring of 16 KB pieces in shared memory, by bulk
+// copies (loads into registers did not get past 4 TB/s, whatever was in flight); eight go through
+// the pieces; one works for them.  In the first pass over a row the eight keep a running maximum and
+// sum per thread (fp32) over the classes outside the list where the list matters (bits in shared
+// memory mark it), so p_rest is a sum of its own and never a difference.  The second pass writes the
+// gradient as one exponential times one factor per class.  It takes the row from L2 again: three CTAs
+// per SM where that many rows stay there, and the next row's first pass before this one's second
+// where twice as many do (see launch()).
 //
 // The one warp has, in between, the list of the row after next (its bits, q, the listed classes'
 // exponentials) and the sums of the last one: what the loss is made of (logarithms and the
 // differences between them, which nearly cancel when the student is close) is fp64, for the listed
 // classes alone.  It also takes the classes of a row that lie outside its 16-byte boundaries, and
 // writes the listed classes' gradient, last, over the others'.
+//
+// What bounds it: HBM.  777 x 50257 fp32 forward: 32 us (4.8 TB/s of logits).  1024 x 32000 fp32 to
+// bf16 gradients: 50 us, the logits and the gradient at 3.9 TB/s; 1024 rows are 2.3 rounds of the 444
+// CTAs.  4096 x 128000 bf16: 503 us, where rows of 256 KB no longer stay in L2 and HBM carries the
+// logits twice and the gradient once, at 6.2 TB/s.  Ways around the second reading lost: a cluster
+// that keeps a row in its shared memory (its reductions, 20 us of a row's life, left HBM idle), and
+// one CTA of 16 warps per SM that keeps what its ring holds (484 us here, but 62 in place of 50 for
+// the smaller rows: the time between the passes is filled by nothing).
 #include <cuda_bf16.h>
 #include <type_traits>
 

@@ -277,6 +277,10 @@ __device__ __forceinline__ void xent_dz32(float (&v)[32], int at, const XentToke
         for (int j = 0; j < 32; ++j)
             if (j == at) v[j] -= 1.f;
     }
+    if (tok.dl == 0.f) {  // whatever its logits are
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= tok.dl;
 }
@@ -308,7 +312,9 @@ __device__ __forceinline__ void xent_columns_t(const XentEpilogue& e, float (&v)
             float x = v[j];
             if constexpr (kEpi == kDz) {
                 const float p = xent_ex2(fmaf(x, kLog2e, -__shfl_sync(0xffffffffu, tok.lse2, j)));
-                x = (p - (__shfl_sync(0xffffffffu, tok.label, j) == cls ? 1.f : 0.f)) * __shfl_sync(0xffffffffu, tok.dl, j);
+                const float dl = __shfl_sync(0xffffffffu, tok.dl, j);
+                x = (p - (__shfl_sync(0xffffffffu, tok.label, j) == cls ? 1.f : 0.f)) * dl;
+                x = dl == 0.f ? 0.f : x;
             }
             if (j < n && there) {
                 if constexpr (kEpi == kPartial) {

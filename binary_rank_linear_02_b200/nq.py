@@ -518,6 +518,20 @@ def _head_types():
             "f32": (torch.float32,), "i32": (torch.int32,), "logits": (torch.float32, torch.bfloat16)}
 
 
+def _new(like, shape, dtype, stream):
+    """An empty tensor on the device of `like`, of the caching allocator's memory for the stream
+    that will write it: on another stream than the current one, memory of the current one's could
+    still be in use there, or be given away there while the call is under way."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+
+    if int(stream) == torch._C._cuda_getCurrentRawStream(like.get_device()):
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=like.device)):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def pack_q4(codes, out=None, stream=None):
     """rows x cols uint8 codes 0 .. 15 (torch tensor or numpy array) -> rows x ceil(cols/8) words."""
     rows, cols = codes.shape
@@ -532,7 +546,7 @@ def pack_q4(codes, out=None, stream=None):
 
         _arg(codes, "codes", (torch.uint8,), (rows, cols))
         if out is None:
-            out = torch.empty((rows, wpr), dtype=torch.int32, device=codes.device)
+            out = _new(codes, (rows, wpr), torch.int32, stream)
     _check(_lib.nq_pack_q4(_ptr(codes), rows, cols, _ptr(out), _stream(stream, codes)), "nq_pack_q4")
     return out
 
@@ -551,7 +565,7 @@ def q4_linear_fwd(x, Wq, scales, m: int, n: int, group: int, zeros=None, y=None,
     sp = _arg(scales, "scales", types["fp16"], groups)
     zp = 0 if zeros is None else _arg(zeros, "zeros", types["fp16"], groups)
     if y is None:
-        y = x.new_empty((batch, m), dtype=types["f32"][0])
+        y = _new(x, (batch, m), types["f32"][0], stream)
         yp = y.data_ptr()
     else:
         yp = _arg(y, "y", types["f32"], (batch, m))
@@ -581,7 +595,7 @@ def distill_topk_fwd(logits, ids, teacher, vocab: int, temperature: float = 1.0,
     teacher's logits / temperature over its whole vocabulary, None: the teacher restricted to its list."""
     tokens, ld, k, kind, zp, ip, up, lp, _ = _distill_args(logits, ids, teacher, teacher_lse, None)
     if loss is None:
-        loss = teacher.new_empty((tokens,))
+        loss = _new(teacher, (tokens,), teacher.dtype, stream)
         op = loss.data_ptr()
     else:
         op = _arg(loss, "loss", _head_types()["f32"], (tokens,))
@@ -595,14 +609,14 @@ def distill_topk_bwd(logits, ids, teacher, vocab: int, dloss, temperature: float
                      dlogits=None, loss=None, stream=None):
     """(dlogits, loss): the gradient of sum_i dloss[i] loss[i] with respect to the logits
     (tokens x ld, torch.bfloat16 unless `dtype` says torch.float32; columns from `vocab` on are
-    zero) and the losses, from one read of the logits.  Arguments as distill_topk_fwd."""
+    zero) and the losses, from one call.  Arguments as distill_topk_fwd."""
     types = _head_types()
     tokens, ld, k, kind, zp, ip, up, lp, wp = _distill_args(logits, ids, teacher, teacher_lse, dloss)
     if dlogits is None:
-        dlogits = logits.new_empty((tokens, ld), dtype=types["logits"][1] if dtype is None else dtype)
+        dlogits = _new(logits, (tokens, ld), types["logits"][1] if dtype is None else dtype, stream)
     gp = _arg(dlogits, "dlogits", types["logits"], (tokens, ld))
     if loss is None:
-        loss = teacher.new_empty((tokens,))
+        loss = _new(teacher, (tokens,), teacher.dtype, stream)
         op = loss.data_ptr()
     else:
         op = _arg(loss, "loss", types["f32"], (tokens,))
@@ -627,11 +641,11 @@ def _xent_scratch_bytes(tokens: int, vocab: int, d: int, backward: int, device: 
     return _lib.nq_linear_cross_entropy_scratch_bytes(tokens, vocab, d, backward)
 
 
-def _xent_scratch(h, tokens: int, vocab: int, d: int, backward: int):
+def _xent_scratch(h, tokens: int, vocab: int, d: int, backward: int, stream):
     """(scratch tensor, its size): the caching allocator's memory, so that calls on other streams
     and captured graphs have their own."""
     size = max(_xent_scratch_bytes(tokens, vocab, d, backward, h.get_device()), 16)
-    return h.new_empty((size,), dtype=_scratch_type()), size
+    return _new(h, (size,), _scratch_type(), stream), size
 
 
 @functools.lru_cache(maxsize=None)
@@ -648,16 +662,16 @@ def linear_cross_entropy_fwd(h, W, labels, loss=None, lse=None, stream=None):
     f32 = _head_types()["f32"]
     tokens, vocab, d, hp, wp, lp = _xent_args(h, W, labels)
     if loss is None:
-        loss = h.new_empty((tokens,), dtype=f32[0])
+        loss = _new(h, (tokens,), f32[0], stream)
         op = loss.data_ptr()
     else:
         op = _arg(loss, "loss", f32, (tokens,))
     if lse is None:
-        lse = h.new_empty((tokens,), dtype=f32[0])
+        lse = _new(h, (tokens,), f32[0], stream)
         ep = lse.data_ptr()
     else:
         ep = _arg(lse, "lse", f32, (tokens,))
-    scratch, size = _xent_scratch(h, tokens, vocab, d, 0)
+    scratch, size = _xent_scratch(h, tokens, vocab, d, 0, stream)
     status = _lib.nq_linear_cross_entropy_fwd(hp, wp, lp, tokens, vocab, d, op, ep, scratch.data_ptr(), size,
                                               _stream(stream, h))
     if status:
@@ -672,9 +686,9 @@ def linear_cross_entropy_bwd(h, W, labels, lse, dloss, need_dh: bool = True, nee
     tokens, vocab, d, hp, wp, lp = _xent_args(h, W, labels)
     bf16 = types["bf16"][0]
     ep, gp = _arg(lse, "lse", types["f32"], (tokens,)), _arg(dloss, "dloss", types["f32"], (tokens,))
-    dh = h.new_empty((tokens, d), dtype=bf16) if need_dh else None
-    dW = h.new_empty((vocab, d), dtype=bf16) if need_dW else None
-    scratch, size = _xent_scratch(h, tokens, vocab, d, 1)
+    dh = _new(h, (tokens, d), bf16, stream) if need_dh else None
+    dW = _new(h, (vocab, d), bf16, stream) if need_dW else None
+    scratch, size = _xent_scratch(h, tokens, vocab, d, 1, stream)
     status = _lib.nq_linear_cross_entropy_bwd(hp, wp, lp, ep, gp, tokens, vocab, d, dh.data_ptr() if need_dh else 0,
                                               dW.data_ptr() if need_dW else 0, scratch.data_ptr(), size, _stream(stream, h))
     if status:

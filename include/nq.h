@@ -351,7 +351,9 @@ int nq_lowrank_linear_fwd_noalloc(const void* x, const uint32_t* Upk, const uint
  * arguments is the caller's `scratch`, so that calls on different streams, and captured
  * graphs, share nothing.  Every pointer is device memory of the current device (else
  * NQ_ERR_PTRKIND), 16-byte aligned (else NQ_ERR_ALIGN); outputs overlap no other buffer of
- * the call; the calls are asynchronous on `stream`.
+ * the call; the calls are asynchronous on `stream`.  (nq_pack_q4 alone is as nq_pack_signs in
+ * all of this.)  Their kernels' waits are bounded: one that gave up is reported by
+ * nq_device_status.
  */
 
 /* Element types of logits and their gradients. */
@@ -413,8 +415,9 @@ int nq_q4_linear_fwd(const void* x, const uint32_t* Wq, const void* scales, cons
  *   vocab : 1 .. 1<<20;  ld : vocab .. 1<<21;  k : 1 .. 1024 (else NQ_ERR_SHAPE);
  *   tokens : 0 (a no-op) .. 2^31-1 (else NQ_ERR_BATCH);  temperature > 0 and finite, types as
  *   above (else NQ_ERR_VALUE).
- * bwd reads the logits from memory once and gives loss and gradient of the same pass: it needs
- * nothing from fwd.  Sums over the vocabulary are fp32, the loss's few logarithms and their
+ * bwd gives loss and gradient in one call: it needs nothing from fwd.  Its second pass over a
+ * row finds the logits in the L2 cache, except where the rows under way are too long for that
+ * (beyond about 200 KB each).  Sums over the vocabulary are fp32, the loss's few logarithms and their
  * differences fp64.  Repeated calls agree bit for bit.
  */
 int nq_distill_topk_fwd(const void* logits, int logits_type, int64_t ld, const int32_t* ids, const float* teacher,
@@ -444,8 +447,7 @@ int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const i
  * rounded once to bfloat16: |error of dh_ij| <= 2^-8 (sum_v |dz_iv W_vj| + |dh_ij|), likewise
  * dW.  The scratch of bwd is bounded: dz exists for a piece of the vocabulary at a time (at
  * most 256 MB, or 256 classes), and dh's sums in fp32 in shares (at most 256 MB, or 4 tokens d
- * bytes).  Repeated calls agree bit for bit.  A bounded device wait that gave up is reported by
- * nq_device_status.
+ * bytes).  Repeated calls agree bit for bit.
  */
 int64_t nq_linear_cross_entropy_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d, int backward);
 int nq_linear_cross_entropy_fwd(const void* h, const void* W, const int32_t* labels, int64_t tokens, int64_t vocab,

@@ -84,6 +84,23 @@ def test_q4_matches_reference(nq, m, n, group, batch, zeros):
     q4_check(y, codes, scales, z, x, n, group)
 
 
+# Matrices of an odd number of 128-column blocks beside even ones, several tiles of a narrow one to
+# a stage, one, three and four stages a tile with the last one full, half full and of a single block.
+Q4_BLOCKS = [
+    (40, 128, 64, 8, True), (4800, 128, 32, 8, True), (5000, 384, 32, 2, True), (2500, 896, 128, 4, False),
+    (700, 2048, 64, 1, True), (333, 4224, 128, 1, False), (650, 6272, 64, 8, True), (2400, 1920, 32, 7, False),
+]
+
+
+@pytest.mark.parametrize("m,n,group,batch,zeros", Q4_BLOCKS)
+def test_q4_blocks_of_a_stage(nq, m, n, group, batch, zeros):
+    codes, scales, z, x = q4_case(m, n, group, batch, zeros, 4000 + m + n)
+    w = nq.pack_q4(codes)
+    y = nq.q4_linear_fwd(x, w, scales, m, n, group, zeros=z)
+    q4_check(y, codes, scales, z, x, n, group)
+    assert torch.equal(y, nq.q4_linear_fwd(x, w, scales, m, n, group, zeros=z))
+
+
 def test_q4_pack_device_equals_host(nq):
     codes = torch.randint(0, 16, (37, 133), device="cuda", generator=gen(5), dtype=torch.uint8)
     got = nq.pack_q4(codes)
@@ -384,6 +401,22 @@ def test_cross_entropy_matches_reference(nq, tokens, vocab, d):
     nq.device_status()
 
 
+# Sums over d in one part, two and three; K blocks fewer than a tile's accumulators (up to 64
+# tokens four, up to 128 two); last column tiles of 1, 128, 129 and 255 classes, with labels in them.
+XENT_PARTS = [
+    (257, 385, 3008), (300, 513, 3136), (385, 767, 5200), (17, 300, 8), (40, 513, 136), (64, 130, 1040), (65, 700, 72),
+    (128, 257, 264), (144, 260, 64), (270, 128, 8),
+]
+
+
+@pytest.mark.parametrize("tokens,vocab,d", XENT_PARTS)
+def test_cross_entropy_parts_of_a_sum(nq, tokens, vocab, d):
+    h, W, labels, dloss = xent_case(tokens, vocab, d, 5000 + tokens + vocab + d)
+    labels[4] = vocab - 1 - (vocab - 1) % 128  # the first class of the last half tile
+    xent_check(nq, h, W, labels, dloss)
+    nq.device_status()
+
+
 def test_cross_entropy_more_than_one_piece(nq):
     """dz of 4100 tokens and 40000 classes does not fit its scratch: the vocabulary in pieces."""
     assert nq.lib().nq_linear_cross_entropy_scratch_bytes(4100, 40000, 64, 1) < 2 * 4100 * 40000
@@ -491,6 +524,37 @@ def test_head_on_two_streams_at_once(nq):
     for i in range(2):
         for a, b in zip(alone[i], got[i]):
             assert torch.equal(a, b)
+
+
+def test_head_on_another_stream_than_the_current(nq):
+    """A call that is given another stream than the current one, which is busy when it comes: its
+    scratch and its results are not the current stream's memory, which is given out and filled
+    again while the call still waits."""
+    h, W, labels, dl = xent_case(300, 4000, 512, 76)
+    codes, scales, z, x = q4_case(2000, 1024, 64, 4, True, 77)
+    w = nq.pack_q4(codes)
+    logits, ids, teacher, tl, dloss = distill_case(64, 9000, 9000, 16, True, 2.0, torch.float32, 78)
+
+    def go(stream=None):
+        loss, lse = nq.linear_cross_entropy_fwd(h, W, labels, stream=stream)
+        dh, dW = nq.linear_cross_entropy_bwd(h, W, labels, lse, dl, stream=stream)
+        y = nq.q4_linear_fwd(x, w, scales, 2000, 1024, 64, zeros=z, stream=stream)
+        dz, dist = nq.distill_topk_bwd(logits, ids, teacher, 9000, dloss, temperature=2.0, teacher_lse=tl, stream=stream)
+        return loss, lse, dh, dW, y, dz, dist
+
+    want = go()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = go(side.cuda_stream)
+        sizes = [nq.lib().nq_linear_cross_entropy_scratch_bytes(300, 4000, 512, b) for b in (0, 1)]
+        filled = [torch.full((s,), 0x7F, dtype=torch.uint8, device="cuda") for s in sizes]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+        del filled
 
 
 def test_head_in_captured_graphs(nq):
