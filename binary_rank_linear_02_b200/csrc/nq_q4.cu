@@ -39,7 +39,7 @@
 //
 // Measured: 32001 x 4096 (groups of 64 with zero points), 1 token: 25 us, 2.9 TB/s; 28672 x 8192
 // (groups of 128), 8 tokens: 37 us, 3.3 TB/s, of which x takes 5 to be brought in and launch and
-// pipeline about as long to start; in between the issue of instructions bounds it, some 170 per 2048
+// pipeline about as long to start; in between instructions bound it, some 180 per 2048
 // weights.  Small matrices take 5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -554,6 +554,7 @@ def test_head_on_another_stream_than_the_current(nq):
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+        assert all(torch.all(f == 0x7F) for f in filled)
         del filled
 
 
