@@ -11,6 +11,7 @@
 // tokens) and its share of dh (summed over the pieces in fp32, in order).  dz in bfloat16 is
 // what lets both products run on the bf16 tensor cores (an operand pair has one type): its
 // rounding is at most 2^-8 of each term, of the same size as the rounding of the bfloat16 results.
+// With few tokens, where these roundings do not average out, dz is two bfloat16 parts.
 //
 // All four products are the same tcgen05 kernel (kind::f16, bf16 operands, fp32 accumulators)
 // with other operand orders and epilogues: dW reads dz and h token-major (MN-major tiles), dh
@@ -141,6 +142,7 @@ struct XentEpilogue {
     const float* dloss;     // kDz, per token
     uint16_t* out;          // kDz, kToBf16: bf16, [row][column] with pitch ldo (kT: [column][row])
     int64_t ldo;
+    int low;                // kDz, kT: what bf16 leaves of dz goes this many columns on (0: nowhere)
     float* part;            // kPartial: [split][row][column] fp32 (kT: [split][column][row]), added to unless first
     int first;
 };
@@ -314,9 +316,15 @@ __device__ __forceinline__ void xent_columns_t(const XentEpilogue& e, float (&v)
                 const float p = xent_ex2(fmaf(x, kLog2e, -__shfl_sync(0xffffffffu, tok.lse2, j)));
                 const float dl = __shfl_sync(0xffffffffu, tok.dl, j);
                 x = (p - (__shfl_sync(0xffffffffu, tok.label, j) == cls ? 1.f : 0.f)) * dl;
-                x = dl == 0.f ? 0.f : x;
+                x = dl == 0.f || j >= n ? 0.f : x;
+                if (e.low && there && col + j < e.low) {  // (columns after the last: zeros)
+                    const __nv_bfloat16 high = __float2bfloat16_rn(x);
+                    e.out[(col + j) * e.ldo + row] = __bfloat16_as_ushort(high);
+                    e.out[(e.low + col + j) * e.ldo + row] =
+                        __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(high)));
+                }
             }
-            if (j < n && there) {
+            if (j < n && there && (kEpi != kDz || !e.low)) {
                 if constexpr (kEpi == kPartial) {
                     float* a = e.part + (split * e.cols + col + j) * e.rows + row;
                     *a = e.first ? x : x + *a;
@@ -389,6 +397,8 @@ struct XentPlan {
     int tm, tn, nkb, per_split, splits;
     int bn, stages;  // columns of a tile (256; transposed a multiple of 16); stages of the ring
     int accs;        // accumulators of a transposed tile, which its K blocks go to in turn
+    int low;         // kT: the second half of a tile's columns is added to the first; not kT: where the second half
+                     // of A's K blocks begins (both 0: no such halves)
     int part;        // K blocks that are summed in tensor memory before the epilogue takes them
     int n_fastest;  // the order of the tiles: neighbours in the first index run at the same time
 };
@@ -475,17 +485,22 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                     const uint32_t full = in_leader(smem_u32(&bar.full[st]));
                     if (rank == 0) mbar_expect_tx(smem_u32(&bar.full[st]), 2u * stage_bytes);
                     const uint32_t dst = base + (uint32_t)st * stage_bytes;
+                    int ak = kb * kXK, bk = ak;  // (the second half of A meets B again)
+                    if (AMN && BMN && plan.low && 2 * kb >= plan.nkb) {
+                        bk = (kb - plan.nkb / 2) * kXK;
+                        ak = plan.low + bk;
+                    }
                     if constexpr (AMN) {
-                        pair_load_2d(dst, &amap, m0, kb * kXK, full);
-                        pair_load_2d(dst + kXBox, &amap, m0 + 64, kb * kXK, full);
+                        pair_load_2d(dst, &amap, m0, ak, full);
+                        pair_load_2d(dst + kXBox, &amap, m0 + 64, ak, full);
                     } else {
-                        pair_load_2d(dst, &amap, kb * kXK, m0, full);
+                        pair_load_2d(dst, &amap, ak, m0, full);
                     }
                     if constexpr (BMN) {
-                        pair_load_2d(dst + kXABytes, &bmap, n0, kb * kXK, full);
-                        pair_load_2d(dst + kXABytes + kXBox, &bmap, n0 + 64, kb * kXK, full);
+                        pair_load_2d(dst + kXABytes, &bmap, n0, bk, full);
+                        pair_load_2d(dst + kXABytes + kXBox, &bmap, n0 + 64, bk, full);
                     } else {
-                        pair_load_2d(dst + kXABytes, &bmap, kb * kXK, n0, full);
+                        pair_load_2d(dst + kXABytes, &bmap, bk, n0, full);
                     }
                     if (++st == stages) {
                         st = 0;
@@ -575,10 +590,11 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                 const uint32_t taddr = tmem + lanes + (uint32_t)(acc * kXTile);
                 if constexpr (kT) {
                     const int accs = kb1 - kb0 < plan.accs ? kb1 - kb0 : plan.accs;
+                    const int columns = plan.low ? plan.low : plan.bn;
 #pragma unroll 1
-                    for (int c0 = 32 * half; c0 < plan.bn; c0 += 64) {
-                        const int64_t col = (int64_t)tn * plan.bn + c0, left = e.cols - col;
-                        const int room = plan.bn - c0 < 32 ? plan.bn - c0 : 32, here = left < room ? (int)left : room;
+                    for (int c0 = 32 * half; c0 < columns; c0 += 64) {
+                        const int64_t col = (int64_t)tn * columns + c0, left = e.cols - col;
+                        const int room = columns - c0 < 32 ? columns - c0 : 32, here = left < room ? (int)left : room;
                         if (here <= 0) break;
                         tok = xent_token<kEpi>(e, col + lane, lane < here);
                         float v[32];
@@ -589,6 +605,13 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j] += w[j];
                         }
+                        if (plan.low)
+                            for (int i = 0; i < accs; ++i) {
+                                float w[32];
+                                xent_load32(taddr + (uint32_t)(i * plan.bn + plan.low + c0), w);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] += w[j];
+                            }
                         xent_columns_t<kEpi>(e, v, row0 + lane, col, here, split, (tm * 2 + (int)rank) * 4 + quad, tok);
                     }
                 } else if constexpr (kKeeps) {
@@ -699,7 +722,7 @@ int64_t cut(int64_t v, int64_t a) { return (v + a - 1) / a; }
 
 template <int kEpi, bool AMN, bool BMN, bool kT>
 int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N, int64_t K, int bn,
-                int splits, bool n_fastest, const XentEpilogue& e, cudaStream_t stream) {
+                int splits, bool n_fastest, const XentEpilogue& e, cudaStream_t stream, int low = 0) {
     static unsigned long long init_mask = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NQ_ERR_CUDA;
@@ -716,7 +739,7 @@ int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, 
         __atomic_fetch_or(&init_mask, bit, __ATOMIC_RELEASE);
     }
     CUtensorMap amap, bmap;
-    if (!(AMN ? xent_map(&amap, A, K, M, lda, kXK) : xent_map(&amap, A, M, K, lda, kXHalfTile)) ||
+    if (!(AMN ? xent_map(&amap, A, AMN && BMN && low ? 2 * low : K, M, lda, kXK) : xent_map(&amap, A, M, K, lda, kXHalfTile)) ||
         !(BMN ? xent_map(&bmap, B, K, N, ldb, kXK) : xent_map(&bmap, B, N, K, ldb, bn / 2)))
         return NQ_ERR_CUDA;
     XentPlan plan;
@@ -726,7 +749,8 @@ int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, 
     plan.stages = (kT ? kXSpace : kXSpace - kXStaging) / (kXABytes + 64 * bn);
     plan.accs = bn <= 64 ? 4 : bn <= 128 ? 2 : 1;
     if (plan.stages > kXMaxStages) plan.stages = kXMaxStages;
-    plan.nkb = (int)cut(K, kXK);
+    plan.nkb = (int)cut(K, kXK) * (AMN && BMN && low ? 2 : 1);
+    plan.low = low;
     plan.per_split = (int)cut(plan.nkb, splits);
     const int parts = (plan.nkb + kXPart / 2) / kXPart;
     plan.part = kEpi == kStats && !kT && parts > 1 ? (int)cut(plan.nkb, parts) : plan.per_split;
@@ -746,10 +770,17 @@ int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, 
 // after each step, and shorter sums lose less (a few 1e-7 of a loss in place of 1e-6).
 constexpr int64_t kXFewTokens = 256;
 int few_columns(int64_t tokens) { return (int)round_up(tokens, 16); }
+// Up to this many, dz is kept as two bf16 parts, the second so many rows after the first (16
+// bits of it: with few tokens the rounding of a token's large terms would not average out).  It
+// costs next to nothing, since HBM bounds the products that read it: dh has twice the columns
+// per tile of W, dW twice the K blocks.
+constexpr int64_t kXTwoParts = 128;
+int low_rows(int64_t tokens) { return tokens <= kXTwoParts ? few_columns(tokens) : 0; }
+int64_t dz_rows(int64_t tokens) { return tokens <= kXTwoParts ? 2 * few_columns(tokens) : tokens; }
 
 // Classes per piece of the backward: as many whole column tiles as dz's scratch holds.
 int64_t piece_classes(int64_t tokens, int64_t vocab) {
-    const int64_t fit = kXPieceBytes / (2 * tokens) / kXTile * kXTile;
+    const int64_t fit = kXPieceBytes / (2 * dz_rows(tokens)) / kXTile * kXTile;
     const int64_t all = round_up(vocab, kXTile);
     return fit < kXTile ? kXTile : fit < all ? fit : all;
 }
@@ -803,7 +834,7 @@ int64_t xent_fwd_scratch_bytes(int64_t tokens, int64_t vocab) {
 
 int64_t xent_bwd_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d) {
     const BackwardPlan p = plan_backward(tokens, vocab, d);
-    return round_up(2 * tokens * p.piece, 256) + (p.direct ? 0 : round_up(4 * p.splits * tokens * d, 256));
+    return round_up(2 * dz_rows(tokens) * p.piece, 256) + (p.direct ? 0 : round_up(4 * p.splits * tokens * d, 256));
 }
 
 // z of tokens and classes (nv rows of W), its epilogue kEpi: stats or dz.
@@ -827,8 +858,9 @@ static int xent_dh(const uint16_t* dz, int64_t piece, const uint16_t* W, int64_t
     if (tokens <= kXFewTokens) {
         e.rows = d;
         e.cols = tokens;
-        return xent_launch<kEpi, true, false, true>(W, d, dz, piece, d, tokens, nv, few_columns(tokens), splits, false, e,
-                                                    stream);
+        const int low = low_rows(tokens);  // (B: the rows of both parts)
+        return xent_launch<kEpi, true, false, true>(W, d, dz, piece, d, low ? 2 * low : tokens, nv,
+                                                    low ? 2 * low : few_columns(tokens), splits, false, e, stream, low);
     }
     e.rows = tokens;
     e.cols = d;
@@ -858,7 +890,7 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
     const BackwardPlan plan = plan_backward(tokens, vocab, d);
     const int64_t piece = plan.piece;
     uint16_t* dz = static_cast<uint16_t*>(scratch);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(2 * tokens * piece, 256));
+    float* part = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(2 * dz_rows(tokens) * piece, 256));
     for (int64_t v0 = 0; v0 < vocab; v0 += piece) {
         const int64_t nv = vocab - v0 < piece ? vocab - v0 : piece;
         XentEpilogue e = {};
@@ -869,6 +901,7 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
         e.dloss = dloss;
         e.out = dz;
         e.ldo = piece;
+        e.low = low_rows(tokens);
         int rc = xent_logits<kDz>(h, W + v0 * d, tokens, nv, d, e, stream);
         if (rc != NQ_OK) return rc;
         if (dW) {
@@ -877,7 +910,7 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
             g.cols = d;
             g.out = dW + v0 * d;
             g.ldo = d;
-            rc = xent_launch<kToBf16, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream);
+            rc = xent_launch<kToBf16, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream, low_rows(tokens));
             if (rc != NQ_OK) return rc;
         }
         if (dh) {

@@ -445,7 +445,7 @@ int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const i
  * Forward: products exact, sums fp32.  Backward: dz passes through bfloat16 (the operand type
  * of the tensor cores beside h and W), sums over classes and tokens are fp32, results are
  * rounded once to bfloat16: |error of dh_ij| <= 2^-8 (sum_v |dz_iv W_vj| + |dh_ij|), likewise
- * dW.  The scratch of bwd is bounded: dz exists for a piece of the vocabulary at a time (at
+ * dW.  Up to 128 tokens dz is two bfloat16 parts: 2^-16 in place of the first 2^-8.  The scratch of bwd is bounded: dz exists for a piece of the vocabulary at a time (at
  * most 256 MB, or 256 classes), and dh's sums in fp32 in shares (at most 256 MB, or 4 tokens d
  * bytes).  Repeated calls agree bit for bit.
  */

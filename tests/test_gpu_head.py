@@ -417,6 +417,26 @@ def test_cross_entropy_parts_of_a_sum(nq, tokens, vocab, d):
     nq.device_status()
 
 
+@pytest.mark.parametrize("tokens,vocab,d", [(1, 1000, 64), (3, 129, 8), (8, 5003, 520), (16, 513, 264), (17, 257, 1000),
+                                            (64, 300, 128), (65, 513, 72), (127, 1000, 264), (128, 700, 136)])
+def test_cross_entropy_few_tokens_round_once(nq, tokens, vocab, d):
+    """Up to 128 tokens dz passes through two bf16 parts: what the first leaves, at most BF of dz, is
+    rounded to the second, so dz is off by BF^2 of itself; the fp32 sums have the terms of both."""
+    h, W, labels, dloss = xent_case(tokens, vocab, d, 6000 + tokens + vocab + d)
+    lse, z, ez, counted = xent_check_forward(nq, h, W, labels)
+    dh, dW = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    dl = torch.where(counted, dloss.double(), 0.0)[:, None]
+    p = torch.exp(z - lse.double()[:, None]) * dl
+    dz = p.clone()
+    rows = torch.arange(tokens, device="cuda")[counted]
+    dz[rows, labels[counted].long()] -= dl[counted, 0]
+    edz = BF * BF * dz.abs() + (2 * ez + 32 * U) * p.abs() + U * dl.abs()
+    for got, a, b, terms in ((dh, (edz, dz), W.double(), vocab), (dW, (edz.T, dz.T), h.double(), tokens)):
+        ref = a[1] @ b
+        before = a[0] @ b.abs() + (terms / 8 + 32) * U * (1 + 2 * BF) * (a[1].abs() @ b.abs())
+        assert torch.all((got.double() - ref).abs() <= before * (1 + BF) + BF * ref.abs() + 1e-38)
+
+
 def test_cross_entropy_more_than_one_piece(nq):
     """dz of 4100 tokens and 40000 classes does not fit its scratch: the vocabulary in pieces."""
     assert nq.lib().nq_linear_cross_entropy_scratch_bytes(4100, 40000, 64, 1) < 2 * 4100 * 40000
