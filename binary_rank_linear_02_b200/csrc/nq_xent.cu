@@ -582,10 +582,9 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
 #pragma unroll 1
             for (int p0 = kb0; p0 < kb1 && ok; p0 += plan.part, ++n) {
                 const int acc = n & 1;
-                if (!mbar_wait(smem_u32(&bar.acc_full[acc]), (uint32_t)(n >> 1) & 1u, abort_flag, status)) {
-                    ok = false;
-                    break;
-                }
+                // (the warp goes on, or gives up, as one)
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar.acc_full[acc]), (uint32_t)(n >> 1) & 1u, abort_flag, status));
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t taddr = tmem + lanes + (uint32_t)(acc * kXTile);
                 if constexpr (kT) {
