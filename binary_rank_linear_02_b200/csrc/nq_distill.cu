@@ -12,28 +12,26 @@
 // Two or three CTAs per SM go from token to token, with the steps of a token hidden behind
 // another's.  One warp streams the rows through a ring of 16 KB pieces in shared memory, by bulk
 // copies (loads into registers did not get past 4 TB/s, whatever was in flight); eight go through
-// the pieces; two work for them.  In the first pass over a row the eight keep a running maximum and
+// the pieces; one works for them.  In the first pass over a row the eight keep a running maximum and
 // sum per thread (fp32) over the classes outside the list where the list matters (bits in shared
 // memory mark it), so p_rest is a sum of its own and never a difference.  The second pass writes the
 // gradient as one exponential times one factor per class.  It takes the row from L2 again: three CTAs
 // per SM where that many rows stay there, and the next row's first pass before this one's second
 // where twice as many do (see launch()).
 //
-// Of the two, one reads the lists, up to three rows ahead (their bits, q, the listed classes'
-// exponentials), the other puts a row's sums together: what the loss is made of (logarithms and the
+// The one warp has, in between, the list of the row after next (its bits, q, the listed classes'
+// exponentials) and the sums of the last one: what the loss is made of (logarithms and the
 // differences between them, which nearly cancel when the student is close) is fp64, for the listed
-// classes alone.  (One warp for both took some 9 us a row, and 50 us in place of 47.6 for the second
-// case below.)  The other also takes the classes of a row that lie outside its 16-byte boundaries, and
+// classes alone.  It also takes the classes of a row that lie outside its 16-byte boundaries, and
 // writes the listed classes' gradient, last, over the others'.
 //
-// What bounds it: HBM.  777 x 50257 fp32 forward: 33 us (4.7 TB/s of logits).  1024 x 32000 fp32 to
-// bf16 gradients: 48 us, the logits and the gradient at 4.1 TB/s; 1024 rows are 2.3 rounds of the 444
+// What bounds it: HBM.  777 x 50257 fp32 forward: 32 us (4.8 TB/s of logits).  1024 x 32000 fp32 to
+// bf16 gradients: 50 us, the logits and the gradient at 3.9 TB/s; 1024 rows are 2.3 rounds of the 444
 // CTAs.  4096 x 128000 bf16: 503 us, where rows of 256 KB no longer stay in L2 and HBM carries the
 // logits twice and the gradient once, at 6.2 TB/s.  Ways around the second reading lost: a cluster
 // that keeps a row in its shared memory (its reductions, 20 us of a row's life, left HBM idle), and
 // one CTA of 16 warps per SM that keeps what its ring holds (484 us here, but 62 in place of 50 for
-// the smaller rows: the time between the passes is filled by nothing); nor did half a row to each CTA
-// of a cluster, which leaves L2 half as many rows to keep, gain anything (541 us).
+// the smaller rows: the time between the passes is filled by nothing).
 #include <cuda_bf16.h>
 #include <type_traits>
 
@@ -45,7 +43,7 @@ namespace {
 
 constexpr int kDtWarps = 8;                        // that go through the rows
 constexpr int kDtFetch = kDtWarps, kDtTeacher = kDtWarps + 1;  // the warps that fetch them, and that read the teacher
-constexpr int kDtThreads = 32 * (kDtWarps + 3);  // (the last one puts the sums together)
+constexpr int kDtThreads = 32 * (kDtWarps + 2);
 constexpr int kDtPiece = 16384;                    // bytes
 constexpr int kDtMaxSlots = 8;
 constexpr int kDtRows = 3;                         // rows a CTA has something of
@@ -202,17 +200,15 @@ struct DistillRow {
     __device__ __forceinline__ int bit(int v) const { return v - head + 8; }  // of class v: a group of 8 is a byte
 };
 
-template <typename TL, typename TG, bool kGrad, int kPerSm>
-__global__ void __launch_bounds__(kDtThreads, kPerSm) distill_kernel(const DistillArgs p) {
+template <typename TL, typename TG, bool kGrad>
+__global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArgs p) {
     constexpr int kGroupBytes = 8 * sizeof(TL), kPieceGroups = kDtPiece / kGroupBytes;
     constexpr int kSixteen = 32 * kDtWarps;               // threads that go through the rows
     constexpr int kPerThread = kPieceGroups / kSixteen;   // groups of 8 classes a thread has of a piece
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ MaxSum warp_part[kDtRows][kDtWarps];
     __shared__ unsigned long long full[kDtMaxSlots], empty[kDtMaxSlots];
-    // of a row: its list is there; its place is free for another's
-    __shared__ unsigned long long ready_bar[kDtRows], free_bar[kDtRows];
-    // its list's bits are there; its first pass is done; its factors are there; its second pass is done
+    // of a row: its list's bits are there; its first pass is done; its factors are there; its second pass is done
     __shared__ unsigned long long listed_bar[kDtRows], summed_bar[kDtRows], factors_bar[kDtRows], graded_bar[kDtRows];
     __shared__ float factor_of[kDtRows], mr_of[kDtRows], scale_of[kDtRows], m_of[kDtRows], edge_z[kDtRows][16];
     __shared__ double qsum_of[kDtRows], cross_of[kDtRows], sl_of[kDtRows];
@@ -238,8 +234,6 @@ __global__ void __launch_bounds__(kDtThreads, kPerSm) distill_kernel(const Disti
         for (int b = 0; b < kDtRows; ++b) {
             mbar_init(smem_u32(&listed_bar[b]), 1);
             mbar_init(smem_u32(&summed_bar[b]), kDtWarps);
-            mbar_init(smem_u32(&ready_bar[b]), 1);
-            mbar_init(smem_u32(&free_bar[b]), 1);
             mbar_init(smem_u32(&factors_bar[b]), 1);
             mbar_init(smem_u32(&graded_bar[b]), kDtWarps);
         }
@@ -285,7 +279,7 @@ __global__ void __launch_bounds__(kDtThreads, kPerSm) distill_kernel(const Disti
         return;
     }
 
-    if (warp >= kDtTeacher) {
+    if (warp == kDtTeacher) {
         const double T = p.temperature, invT = 1.0 / T;
         auto rounded = [&](float m) { return m > -INFINITY && !far(m, c) ? exp2((double)at(m, c) - (double)m * c) : 1.0; };
         // ---- the list of row i: bits, owners of a class (its first marker), q, what it comes to
@@ -458,28 +452,16 @@ __global__ void __launch_bounds__(kDtThreads, kPerSm) distill_kernel(const Disti
                 if (sid[k] >= 0) mask[r.bit(sid[k]) >> 5] = 0;
             __syncwarp();
         };
-        // One warp reads the lists, up to three rows ahead; one puts the rows' sums together.
-        if (warp == kDtTeacher) {
-            for (int i = 0; i < n; ++i) {
-                const int b = i % kDtRows;
-                if (i >= kDtRows)
-                    mbar_wait(smem_u32(&free_bar[b]), (uint32_t)(i / kDtRows - 1) & 1u, abort_flag, &g_distill_status);
-                read_list(i);
-                if (lane == 0) mbar_arrive(smem_u32(&ready_bar[b]));
-            }
-        } else {
-            auto done = [&](int i) {
-                finish(i);
-                if (lane == 0) mbar_arrive(smem_u32(&free_bar[i % kDtRows]));
-            };
-            for (int i = 0; i < n; ++i) {
-                mbar_wait(smem_u32(&ready_bar[i % kDtRows]), (uint32_t)(i / kDtRows) & 1u, abort_flag, &g_distill_status);
-                put_together(i);
-                if (!kGrad) done(i);
-                if (kGrad && i > 0) done(i - 1);
-            }
-            if (kGrad) done(n - 1);
+        // The row after next's list is read while the sixteen are in the rows before it.
+        read_list(0);
+        if (n > 1) read_list(1);
+        for (int i = 0; i < n; ++i) {
+            put_together(i);
+            if (kGrad && i > 0) finish(i - 1);
+            if (!kGrad) finish(i);
+            if (i + 2 < n) read_list(i + 2);
         }
+        if (kGrad) finish(n - 1);
         __syncthreads();
         return;
     }
@@ -615,23 +597,24 @@ __global__ void __launch_bounds__(kDtThreads, kPerSm) distill_kernel(const Disti
     __syncthreads();
 }
 
-template <typename TL, typename TG, bool kGrad, int kPerSm>
-int launch_as(DistillArgs a, cudaStream_t stream) {
+template <typename TL, typename TG, bool kGrad>
+int launch(DistillArgs a, cudaStream_t stream) {
     static unsigned long long init_mask = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NQ_ERR_CUDA;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(__atomic_load_n(&init_mask, __ATOMIC_ACQUIRE) & bit)) {
-        if (cudaFuncSetAttribute(distill_kernel<TL, TG, kGrad, kPerSm>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(distill_kernel<TL, TG, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kDtMost) != cudaSuccess)
             return NQ_ERR_CUDA;
         __atomic_fetch_or(&init_mask, bit, __ATOMIC_RELEASE);
     }
+    // CTAs per SM: three, or two where that many rows leave L2 between their passes
     const size_t list = distill_list_bytes(a.vocab, a.k);
     const int64_t row_bytes = (int64_t)a.vocab * (int64_t)sizeof(TL);
+    int per_sm = !kGrad || 3 * sm_count() * row_bytes <= kDtStays ? 3 : 2;
     // the lists of three rows beside four pieces at least; of one row, and one row per CTA, where the
     // bits of the vocabulary are too many
-    int per_sm = kPerSm;
     a.rows = kDtRows;
     while (per_sm > 1 && kDtRows * list + 3 * kDtPiece > kDtMost / per_sm - 2048) --per_sm;
     if (kDtRows * list + 3 * kDtPiece > kDtMost / per_sm - 2048) a.rows = 1;
@@ -640,19 +623,10 @@ int launch_as(DistillArgs a, cudaStream_t stream) {
     // a row's second pass after the next row's first, where twice the rows stay in L2
     a.lag = kGrad && 2 * per_sm * sm_count() * row_bytes <= kDtStays;
     const int64_t at_once = (int64_t)per_sm * sm_count(), ctas = a.rows == 1 || a.tokens < at_once ? a.tokens : at_once;
-    return launch_pdl(distill_kernel<TL, TG, kGrad, kPerSm>, dim3((unsigned)ctas), dim3(kDtThreads),
+    return launch_pdl(distill_kernel<TL, TG, kGrad>, dim3((unsigned)ctas), dim3(kDtThreads),
                       (size_t)a.slots * kDtPiece + a.rows * list, stream, a) == cudaSuccess
                ? NQ_OK
                : NQ_ERR_CUDA;
-}
-
-template <typename TL, typename TG, bool kGrad>
-int launch(const DistillArgs& a, cudaStream_t stream) {
-    // CTAs per SM: three, or two (of more registers) where that many rows leave L2 between their passes
-    const int64_t row_bytes = (int64_t)a.vocab * (int64_t)sizeof(TL);
-    if constexpr (kGrad)
-        if (3 * sm_count() * row_bytes > kDtStays) return launch_as<TL, TG, kGrad, 2>(a, stream);
-    return launch_as<TL, TG, kGrad, 3>(a, stream);
 }
 
 }  // namespace
