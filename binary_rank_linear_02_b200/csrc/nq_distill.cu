@@ -25,13 +25,16 @@
 // classes alone.  It also takes the classes of a row that lie outside its 16-byte boundaries, and
 // writes the listed classes' gradient, last, over the others'.
 //
-// What bounds it: HBM.  777 x 50257 fp32 forward: 32 us (4.8 TB/s of logits).  1024 x 32000 fp32 to
+// What bounds it: HBM.  (Device times of a call by itself.)  777 x 50257 fp32 forward: 33 us (4.7 TB/s of logits).  1024 x 32000 fp32 to
 // bf16 gradients: 50 us, the logits and the gradient at 3.9 TB/s; 1024 rows are 2.3 rounds of the 444
 // CTAs.  4096 x 128000 bf16: 503 us, where rows of 256 KB no longer stay in L2 and HBM carries the
 // logits twice and the gradient once, at 6.2 TB/s.  Ways around the second reading lost: a cluster
 // that keeps a row in its shared memory (its reductions, 20 us of a row's life, left HBM idle), and
 // one CTA of 16 warps per SM that keeps what its ring holds (484 us here, but 62 in place of 50 for
-// the smaller rows: the time between the passes is filled by nothing).
+// the smaller rows: the time between the passes is filled by nothing); nor did half a row to each CTA
+// of a cluster, which leaves L2 half as many rows to keep, gain anything (541 us).  A second warp
+// for the teacher (lists by one, sums by the other) made a call by itself 4% faster and calls in a
+// row 1% slower.
 #include <cuda_bf16.h>
 #include <type_traits>
 
