@@ -578,6 +578,20 @@ def test_head_on_another_stream_than_the_current(nq):
         del filled
 
 
+def test_head_on_the_default_stream_from_another(nq):
+    """stream=0 names the default stream, whichever is current."""
+    h, W, labels, dl = xent_case(60, 700, 128, 79)
+    loss, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = nq.linear_cross_entropy_fwd(h, W, labels, stream=0)
+        grads = nq.linear_cross_entropy_bwd(h, W, labels, lse, dl, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], loss) and torch.equal(got[1], lse)
+    for a, b in zip(grads, nq.linear_cross_entropy_bwd(h, W, labels, lse, dl)):
+        assert torch.equal(a, b)
+
+
 def test_head_in_captured_graphs(nq):
     """Two graphs that hold the head's calls, replayed in turn with new inputs and with larger
     eager calls in between."""
