@@ -498,7 +498,10 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
         const DistillRow<TL> r(p, s);
         const int b = s % kDtRows;
         const unsigned char* bytes = reinterpret_cast<const unsigned char*>(mask_of(b)) + 1;
-        if (whole) mbar_wait(smem_u32(&listed_bar[b]), (uint32_t)(s / kDtRows) & 1u, abort_flag, &g_distill_status);
+        auto listed_yet = [&]() {
+            mbar_wait(smem_u32(&listed_bar[b]), (uint32_t)(s / kDtRows) & 1u, abort_flag, &g_distill_status);
+        };
+        if (whole) listed_yet();
         MaxSum sum{-INFINITY, 0.f};
         through(r, [&](const TL* at8, int i, auto count) {
             constexpr int kCount = decltype(count)::value;
@@ -549,6 +552,11 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             sum = join(sum, MaxSum{__shfl_xor_sync(0xffffffffu, sum.m, o), __shfl_xor_sync(0xffffffffu, sum.s, o)}, c);
+        // Only this holds a forward back behind the teacher's warp (a gradient's second passes do as
+        // well): row s's list is read after row s - 2's sums were put together, so the place of row
+        // s - 3's sums is free, and its barrier has been looked at.  Without the list's bits it is
+        // enough to wait here, when the row has been gone through.
+        if (!whole) listed_yet();
         if (lane == 0) {
             warp_part[b][warp] = sum;
             mbar_arrive(smem_u32(&summed_bar[b]));
