@@ -117,22 +117,25 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // A maximum m and a sum s of exponentials relative to it, exactly: the sum of 2^(v c) over what
-// was taken is s 2^at(m), where at(m) is the float m c (0 without values, m = -inf).  One FMA per
-// value; what at() and c round away is made up for in fp64 at the end.  Where m c is near the end
-// of the floats (a mask of the type's lowest value), at(m) stands for the number m c, and only
-// differences (v - m) c are formed.
+// was taken is s 2^ref(m).  ref(m) is the float at(m), m c rounded (0 without values, m = -inf):
+// one FMA per value; what at() and c round away is made up for in fp64 at the end.  It grows with
+// m c, though, and from |m c| = 2^20 on (a mask of -1e10 or the type's lowest value, a tiny
+// temperature) ref(m) is the number m c itself, and only differences (v - m) c are formed: a group
+// of masked classes has that maximum, and at -1e10 the FMA's rest would be 2^439.
 struct MaxSum {
     float m, s;
 };
 // (a product of its own: an FMA that took it in would be another reference)
 __device__ __forceinline__ float at(float m, float c) { return m == -INFINITY ? 0.f : __fmul_rn(m, c); }
-__device__ __forceinline__ bool far(float m, float c) { return m > -INFINITY && !(fabsf(m * c) < 1e30f); }
-__device__ __forceinline__ float ex2_from(float v, float m, float c) {  // 2^(v c - at(m))
+__device__ __forceinline__ bool far(float m, float c) { return m > -INFINITY && !(fabsf(m * c) < 0x1p20f); }
+__device__ __forceinline__ float ex2_from(float v, float m, float c) {  // 2^(v c - ref(m))
     return ex2(far(m, c) ? (v - m) * c : fmaf(v, c, -at(m, c)));
 }
-__device__ __forceinline__ float ex2_between(float a, float b, float c) {  // 2^(at(a) - at(b)), a <= b; 0 for a = -inf
+__device__ __forceinline__ float ex2_between(float a, float b, float c) {  // 2^(ref(a) - ref(b)), a <= b; 0 for a = -inf
     if (a == -INFINITY) return 0.f;
-    return ex2(far(a, c) || far(b, c) ? (a - b) * c : at(a, c) - at(b, c));
+    if (!far(a, c) && !far(b, c)) return ex2(at(a, c) - at(b, c));
+    const float rest_a = far(a, c) ? 0.f : fmaf(a, c, -at(a, c)), rest_b = far(b, c) ? 0.f : fmaf(b, c, -at(b, c));
+    return ex2((a - b) * c - rest_a + rest_b);
 }
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
     const float m = fmaxf(a.m, b.m);
@@ -390,9 +393,8 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             // (in fp64: one exponential's error would shift every logarithm below; an edge class's sum
             // of 1 is relative to its own value, not to at() of it)
             const bool single = lane >= kDtWarps;
-            const double between = single || far(s.m, c) || far(mr, c)
-                                       ? ((double)s.m - mr) * c + (far(mr, c) ? 0.0 : (double)mr * c - at(mr, c))
-                                       : (double)at(s.m, c) - at(mr, c);
+            const double between = (single || far(s.m, c) ? (double)s.m * c : (double)at(s.m, c)) -
+                                   (far(mr, c) ? (double)mr * c : (double)at(mr, c));
             const double off = rounded(mr), sr = off * warp_sum(s.s * (s.m > -INFINITY ? exp2(between) : 0.0));
             const float ml = ml_of[b], m = fmaxf(mr, ml);
             const double qsum = qsum_of[b];

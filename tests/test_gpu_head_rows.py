@@ -65,7 +65,9 @@ def reference(logits, ids, teacher, lse, vocab, t, dloss):
         log_rest = torch.logsumexp(torch.where(out, logp, -torch.inf), 1)
         rest = torch.where(there, (1 - q.sum(1)).clamp_min(0), 0.0)
         loss = loss + torch.where(rest > 0, rest * (rest.clamp_min(1e-300).log() - log_rest), 0.0)
-        share = torch.where(out & there[:, None], (logp - log_rest[:, None]).exp() * rest[:, None], 0.0)
+        # p_v / p_rest is a softmax of the classes outside the list (of logits of -1e20, p_v and p_rest
+        # differ by less than 64 bits of their logarithms hold)
+        share = torch.where(there[:, None], torch.softmax(torch.where(out, z, -torch.inf), 1), 0.0) * rest[:, None]
     tot = (q.sum(1) + rest)[:, None]
     w = (dloss.double() * t)[:, None]
     grad, mag = w * (p * tot - dq - share), w * (p * tot + dq + share)
@@ -121,3 +123,68 @@ def test_distill_rows_alone_and_among_others(nq, rest):
         for a, b in zip(whole, both(slice(i, i + 1))):
             assert torch.equal(a[i:i + 1], b)
     nq.device_status()
+
+
+MASKS = [-1e4, -65504.0, -1e9, -1e10, -3e10, -1e12, -1e20, -1e29, -1e30, -3e38]
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value", MASKS)
+def test_distill_finite_masks(nq, value, dtype, rest):
+    """Masked classes hold some large negative number: they have no part in the row, whether a few
+    are masked, or all but a few, or all that are not listed; a row begins with masked or other classes."""
+    vocab, t, k, tokens = 5003, 1.0, 12, 24
+    logits, ids, teacher, lse, dloss = case(tokens, vocab, vocab, k, rest, t, dtype, 501)
+    g = torch.Generator(device="cuda").manual_seed(502)
+    ids = torch.randint(0, 2500, (tokens, k), device="cuda", generator=g, dtype=torch.int32)
+    for i in range(tokens):
+        if i % 4 == 0:
+            logits[i, 2500:] = value
+        elif i % 4 == 1:
+            logits[i, 2500:4990] = value
+            logits[i, ::2] = value
+            ids[i] |= 1
+        elif i % 4 == 2:
+            logits[i, 1:] = value
+            ids[i] = 0
+        else:
+            kept = logits[i, ids[i].long()].clone()
+            logits[i] = value
+            logits[i, ids[i].long()] = kept
+    if rest:  # a teacher whose mass is all but in its list (what is masked here has next to none there)
+        lse = torch.logsumexp(teacher.double() / t, 1).float() + 1e-3
+    loss, grad, mag = reference(logits, ids, teacher, lse, vocab, t, dloss)
+    e = (vocab / 512 + 96) * U
+    got = nq.distill_topk_fwd(logits, ids, teacher, vocab, temperature=t, teacher_lse=lse)
+    dz, loss2 = nq.distill_topk_bwd(logits, ids, teacher, vocab, dloss, temperature=t, teacher_lse=lse, dtype=torch.float32)
+    for x in (got, loss2):
+        assert torch.all((x.double() - loss).abs() <= t * t * 2 * e + U * loss.abs())
+    assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 1e-38)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("t", [2.0 ** -28, 2.0 ** -20, 2.0 ** -13])
+def test_distill_small_temperatures(nq, t, rest):
+    """logits / temperature of up to 5e9: a rounding of it would be a power of two of its own.  (Powers
+    of two: the temperature reaches the kernel as fp32.)"""
+    vocab = 2003
+    logits, ids, teacher, lse, dloss = case(40, vocab, vocab, 8, rest, 1.0, torch.float32, 503)
+    # differences of a few temperatures between some of the classes, so that a row has several terms
+    g = torch.Generator(device="cuda").manual_seed(504)
+    logits = torch.randn(40, vocab, device="cuda", generator=g) * 3 * t
+    logits[1::2, ::3] += 20.0  # two levels, far from each other
+    logits[3::4] -= 7.0
+    if rest:
+        lse = torch.logsumexp(teacher.double() / t, 1).float()
+        teacher = torch.full_like(teacher, -t)
+        lse = torch.full_like(lse, 1.5)
+    else:
+        teacher = teacher * t
+    loss, grad, mag = reference(logits, ids, teacher, lse, vocab, t, dloss)
+    e = (vocab / 512 + 96) * U
+    got = nq.distill_topk_fwd(logits, ids, teacher, vocab, temperature=t, teacher_lse=lse)
+    dz, loss2 = nq.distill_topk_bwd(logits, ids, teacher, vocab, dloss, temperature=t, teacher_lse=lse, dtype=torch.float32)
+    for x in (got, loss2):
+        assert torch.all((x.double() - loss).abs() <= t * t * 2 * e + U * loss.abs())
+    assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 1e-38)
