@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
     __shared__ unsigned long long listed_bar[kDtRows], summed_bar[kDtRows], factors_bar[kDtRows], graded_bar[kDtRows];
     __shared__ float factor_of[kDtRows], mr_of[kDtRows], scale_of[kDtRows], m_of[kDtRows], edge_z[kDtRows][16];
     __shared__ double qsum_of[kDtRows], cross_of[kDtRows], sl_of[kDtRows];
-    __shared__ float ml_of[kDtRows];
+    __shared__ float ml_of[kDtRows], origin_of[kDtRows];
     __shared__ int any_of[kDtRows], dups_of[kDtRows], abort_word;
     volatile int* abort_flag = &abort_word;
     const int V = p.vocab, K = p.k, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             if (lane < r.edge) edge_z[b][lane] = load1(r.z + r.edge_class(lane));
             bool any = false, twice = false;
             double umax = -INFINITY;
+            float zmax = -INFINITY;
             constexpr int kBatch = 4;
             for (int k0 = lane; k0 < K + lane; k0 += 32 * kBatch) {
                 int id[kBatch];
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                         twice |= !own;
                         any = true;
                         umax = fmax(umax, (double)uk[j]);
+                        zmax = fmaxf(zmax, zk[j]);
                     }
                     sid[k] = id[j];
                     sz[k] = zk[j];
@@ -345,11 +347,15 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                 umax = warp_max(umax);
                 shift = umax * invT;
             }
+            // the logits' part of the loss is taken from the largest listed one on: where a whole row
+            // is at -1e20, log p is what is left when that goes
+            zmax = (float)warp_max(zmax);
+            const float origin = fabsf(zmax) < INFINITY ? zmax : 0.f;
             for (int k = lane; k < K; k += 32) {
                 const double lq = sq[k] * invT - shift, q = sid[k] >= 0 ? exp(lq) : 0.0;
                 sq[k] = q;
                 qsum += q;
-                if (q > 0.0) cross += q * (lq - (double)sz[k] * invT);
+                if (q > 0.0) cross += q * (lq - ((double)sz[k] - origin) * invT);
                 if (whole && owner[k]) ml = fmaxf(ml, sz[k]);
             }
             qsum = warp_sum(qsum);
@@ -370,6 +376,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                 cross_of[b] = cross;
                 sl_of[b] = sl;
                 ml_of[b] = ml;
+                origin_of[b] = origin;
                 any_of[b] = any;
                 dups_of[b] = twice;
             }
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                 double loss = 0.0;  // with nothing to learn from, whatever the logits are
                 if (any_of[b]) {
                     const double logsum = log(sum);  // log p_v = (z_v - m) / T - logsum
-                    loss = cross_of[b] + qsum * (m * invT + logsum);
+                    loss = cross_of[b] + qsum * (((double)m - origin_of[b]) * invT + logsum);
                     if (qrest > 0.0) loss += qrest * (log(qrest) - (((double)mr - m) * invT + log(sr) - logsum));
                 }
                 p.loss[r.row] = (float)(loss * T * T);

@@ -188,3 +188,25 @@ def test_distill_small_temperatures(nq, t, rest):
     for x in (got, loss2):
         assert torch.all((x.double() - loss).abs() <= t * t * 2 * e + U * loss.abs())
     assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 1e-38)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value", [-1e20, -3e38, 3e38, 1e12, -1e6])
+def test_distill_rows_at_one_large_value(nq, value, dtype, rest):
+    """Rows whose mask leaves nothing but its own value, which is a uniform distribution, and rows
+    of which a half is left at it."""
+    vocab, t, k, tokens = 2047, 2.0, 8, 9
+    logits, ids, teacher, lse, dloss = case(tokens, vocab, vocab, k, rest, t, dtype, 505)
+    logits[:] = value
+    logits[::3, 1000:] = -1e30 if value > -1e30 else float("-inf")
+    ids[::3] = ids[::3] % 1000
+    if rest:
+        lse = torch.logsumexp(teacher.double() / t, 1).float() + 0.2
+    loss, grad, mag = reference(logits, ids, teacher, lse, vocab, t, dloss)
+    e = (vocab / 512 + 96) * U
+    got = nq.distill_topk_fwd(logits, ids, teacher, vocab, temperature=t, teacher_lse=lse)
+    dz, loss2 = nq.distill_topk_bwd(logits, ids, teacher, vocab, dloss, temperature=t, teacher_lse=lse, dtype=torch.float32)
+    for x in (got, loss2):
+        assert torch.all((x.double() - loss).abs() <= t * t * 2 * e + U * loss.abs())
+    assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 1e-38)
