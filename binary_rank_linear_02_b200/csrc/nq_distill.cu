@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
     if (warp == kDtTeacher) {
         const double T = p.temperature, invT = 1.0 / T;
         auto rounded = [&](float m) { return m > -INFINITY && !far(m, c) ? exp2((double)at(m, c) - (double)m * c) : 1.0; };
-        // ---- the list of row i: bits, owners of a class (its first marker), q, what it comes to
+        // ---- the list of row i: bits, owners of a class (its first entry), q, what it comes to
         auto read_list = [&](int i) {
             const DistillRow<TL> r(p, i);
             const int b = i % kDtRows;
@@ -321,16 +321,21 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
                     const int k = k0 + 32 * j;
-                    if (k >= K) continue;
+                    if (k - lane >= K) break;
+                    // (a class belongs to its first entry in the list, whichever lane is faster: the
+                    // order of the sum over the classes follows)
+                    const bool first = !(__match_any_sync(0xffffffffu, id[j]) & ((1u << lane) - 1u));
                     bool own = false;
                     if (id[j] >= 0) {
                         const int bit = r.bit(id[j]);
-                        own = !(atomicOr(&mask[bit >> 5], 1u << (bit & 31)) >> (bit & 31) & 1u);
+                        own = first && !(atomicOr(&mask[bit >> 5], 1u << (bit & 31)) >> (bit & 31) & 1u);
                         twice |= !own;
                         any = true;
                         umax = fmax(umax, (double)uk[j]);
                         zmax = fmaxf(zmax, zk[j]);
                     }
+                    __syncwarp();
+                    if (k >= K) continue;
                     sid[k] = id[j];
                     sz[k] = zk[j];
                     owner[k] = own;

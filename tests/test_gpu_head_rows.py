@@ -210,3 +210,29 @@ def test_distill_rows_at_one_large_value(nq, value, dtype, rest):
     for x in (got, loss2):
         assert torch.all((x.double() - loss).abs() <= t * t * 2 * e + U * loss.abs())
     assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 1e-38)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_lists_of_repeated_ids(nq, rest):
+    """Lists in which every class stands several times, next to itself and far from it: against the
+    definitions, and the same bits each time (the order of no sum is left to the lanes' speed)."""
+    vocab, t, k, tokens = 300, 1.0, 1024, 600
+    logits, _, _, _, dloss = case(tokens, vocab, vocab, 1, rest, t, torch.float32, 506)
+    g = torch.Generator(device="cuda").manual_seed(507)
+    ids = torch.randint(-2, vocab, (tokens, k), device="cuda", generator=g, dtype=torch.int32)
+    ids[::2, 1::2] = ids[::2, ::2]
+    teacher = torch.randn(tokens, k, device="cuda", generator=g)
+    lse = torch.logsumexp(teacher.double() / t, 1).float() + 0.3 if rest else None
+    loss, grad, mag = reference(logits, ids, teacher, lse, vocab, t, dloss)
+    e = (vocab / 512 + 96) * U
+    first = None
+    for _ in range(30):
+        got = nq.distill_topk_fwd(logits, ids, teacher, vocab, temperature=t, teacher_lse=lse)
+        dz, loss2 = nq.distill_topk_bwd(logits, ids, teacher, vocab, dloss, temperature=t, teacher_lse=lse, dtype=torch.float32)
+        if first is None:
+            first = got, dz, loss2
+            # (a sum of up to k masses per class beside the terms' own rounding)
+            assert torch.all((got.double() - loss).abs() <= t * t * 2 * e + U * loss.abs())
+            assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 1e-38)
+        for a, b in zip(first, (got, dz, loss2)):
+            assert torch.equal(a, b)
