@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <mutex>
 #include <vector>
+#include <float.h>
 #include <string.h>
 
 #include "nq_internal.cuh"
@@ -1018,7 +1019,7 @@ static int check_distill(int logits_type, int64_t ld, int64_t tokens, int64_t vo
     if (tokens < 0 || tokens > kMaxRows) return NQ_ERR_BATCH;
     if (vocab <= 0 || vocab > kMaxDim || ld < vocab || ld > 2 * kMaxDim || k <= 0 || k > kMaxListed) return NQ_ERR_SHAPE;
     if (logits_type != NQ_F32 && logits_type != NQ_BF16) return NQ_ERR_VALUE;
-    if (!(temperature > 0.f) || temperature > 3.4e38f) return NQ_ERR_VALUE;
+    if (!(temperature >= FLT_MIN && temperature <= FLT_MAX)) return NQ_ERR_VALUE;  // (below, 1 / temperature overflows)
     return NQ_OK;
 }
 

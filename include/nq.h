@@ -413,8 +413,8 @@ int nq_q4_linear_fwd(const void* x, const uint32_t* Wq, const void* scales, cons
  *   dlogits : rows as the logits' (same ld), of grad_type; columns vocab .. ld-1 are written
  *             with 0, so that it can be the dy of a padded factorised head
  *   vocab : 1 .. 1<<20;  ld : vocab .. 1<<21;  k : 1 .. 1024 (else NQ_ERR_SHAPE);
- *   tokens : 0 (a no-op) .. 2^31-1 (else NQ_ERR_BATCH);  temperature > 0 and finite, types as
- *   above (else NQ_ERR_VALUE).
+ *   tokens : 0 (a no-op) .. 2^31-1 (else NQ_ERR_BATCH);  temperature : a positive normal fp32
+ *   number (2^-126 at least); types as above (else NQ_ERR_VALUE).
  * bwd gives loss and gradient in one call: it needs nothing from fwd.  Its second pass over a
  * row finds the logits in the L2 cache, except where the rows under way are too long for that
  * (beyond about 200 KB each).  Sums over the vocabulary are fp32, the loss's few logarithms and their

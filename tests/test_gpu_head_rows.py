@@ -236,3 +236,20 @@ def test_distill_lists_of_repeated_ids(nq, rest):
             assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 1e-38)
         for a, b in zip(first, (got, dz, loss2)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("t", [2.0 ** -126, 2.0 ** 40])
+def test_distill_temperatures_at_the_ends(nq, t, rest):
+    """Each row's largest logit has all the mass, or all classes have the same."""
+    vocab = 777
+    logits, ids, teacher, _, dloss = case(30, vocab, vocab, 6, rest, 1.0, torch.float32, 508)
+    teacher = torch.randn(30, 6, device="cuda", generator=torch.Generator(device="cuda").manual_seed(509)) * t
+    lse = torch.full((30,), 2.5, device="cuda") if rest else None
+    loss, grad, mag = reference(logits, ids, teacher, lse, vocab, t, dloss)
+    e = (vocab / 512 + 96) * U
+    dz, got = nq.distill_topk_bwd(logits, ids, teacher, vocab, dloss, temperature=t, teacher_lse=lse, dtype=torch.float32)
+    # (fp32 numbers below 2^-126 are 2^-149 apart: a result there is rounded by up to 2^-150, which no
+    # multiple of it bounds; a gradient's factors there, of which there are some, may be flushed to 0)
+    assert torch.all((got.double() - loss).abs() <= t * t * 2 * e + U * loss.abs() + 2.0 ** -150)
+    assert torch.all((dz.double() - grad).abs() <= 3 * e * mag + U * grad.abs() + 2.0 ** -126)
