@@ -1,12 +1,14 @@
 // nq_api.cu -- the C ABI of libnq (declared in include/nq.h): argument checks, the
 // per-device workspace, host-memory staging and the decode / prefill dispatch.
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <vector>
 #include <float.h>
 #include <string.h>
 
 #include "nq_internal.cuh"
+#include "nq_sm100.cuh"
 
 namespace nq {
 
@@ -19,6 +21,7 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;  // element-wise helpers: elemen
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;  // one CTA per row
 constexpr int64_t kMaxListed = 1024;                  // teacher entries per token
 constexpr int64_t kMaxXentTokens = int64_t(1) << 24;
+std::atomic<unsigned long long> g_head_wait_ns{kWaitLimitNs};
 // From this many tokens the factor gradients take the prefill GEMM for t and u and the
 // tensor cores for the sums over the tokens; below, the decode stage 1 and a SIMT kernel.
 constexpr int64_t kFactorTcMinBatch = 64;
@@ -76,6 +79,8 @@ int pointer_kind_pinned(const void* p, void** pinned) {
 }
 
 }  // namespace
+
+unsigned long long head_wait_ns() { return g_head_wait_ns.load(std::memory_order_relaxed); }
 
 int sm_count() {
     int dev = 0;
@@ -848,6 +853,12 @@ int nq_selftest_wait_timeout(int64_t limit_ns, void* stream) {
     Workspace* ws = workspace_for(128, 128, 128, 0, DecodeNeed(), &st);
     if (!ws) return st;
     return selftest_wait_timeout(limit_ns, ws, static_cast<cudaStream_t>(stream));
+}
+
+int nq_selftest_head_wait_limit(int64_t limit_ns) {
+    if (limit_ns < 0 || limit_ns > 10000000000ll) return NQ_ERR_VALUE;
+    g_head_wait_ns.store(limit_ns ? (unsigned long long)limit_ns : kWaitLimitNs, std::memory_order_relaxed);
+    return NQ_OK;
 }
 
 int nq_workspace_reserve(int64_t m, int64_t n, int64_t r, int64_t batch) {

@@ -70,6 +70,7 @@ struct DistillArgs {
     int64_t tokens;
     int slots, rows;           // pieces of shared memory; rows of lists in it
     int lag;                   // first passes ahead of the second ones (0, 1)
+    unsigned long long wait_ns;  // kTimed: how long a wait lasts
 };
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -206,8 +207,10 @@ struct DistillRow {
     __device__ __forceinline__ int bit(int v) const { return v - head + 8; }  // of class v: a group of 8 is a byte
 };
 
-template <typename TL, typename TG, bool kGrad>
+// (kTimed: a kernel of its own, since a limit that is not a constant costs the others 1%)
+template <typename TL, typename TG, bool kGrad, bool kTimed>
 __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArgs p) {
+    const unsigned long long limit_ns = kTimed ? p.wait_ns : kWaitLimitNs;
     constexpr int kGroupBytes = 8 * sizeof(TL), kPieceGroups = kDtPiece / kGroupBytes;
     constexpr int kSixteen = 32 * kDtWarps;               // threads that go through the rows
     constexpr int kPerThread = kPieceGroups / kSixteen;   // groups of 8 classes a thread has of a piece
@@ -260,7 +263,8 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             auto stream = [&](int i) {
                 const DistillRow<TL> r(p, i);
                 for (int first = 0; first < r.groups && ok; first += kPieceGroups) {
-                    ok = mbar_wait(smem_u32(&empty[slot]), phase ^ 1u, abort_flag, &g_distill_status);
+                    // (a warp that gave up frees pieces without having waited for them)
+                    ok = mbar_wait(smem_u32(&empty[slot]), phase ^ 1u, abort_flag, &g_distill_status, limit_ns) && !*abort_flag;
                     if (!ok) break;
                     const uint32_t bytes = (uint32_t)((r.groups - first < kPieceGroups ? r.groups - first : kPieceGroups) * kGroupBytes);
                     const uint32_t bar = smem_u32(&full[slot]);
@@ -277,9 +281,9 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                 if (s < n) stream(s);
                 if (kGrad && s >= p.lag) stream(s - p.lag);
             }
-            if (!ok)  // given up: what is in flight lands before the CTA leaves
-                for (int i = issued - p.slots < 0 ? 0 : issued - p.slots; i < issued; ++i)
-                    mbar_drain(smem_u32(&full[i % p.slots]), (uint32_t)(i / p.slots) & 1u);
+            // whoever gave up, if any: what is in flight lands before the CTA leaves
+            for (int i = issued - p.slots < 0 ? 0 : issued - p.slots; i < issued; ++i)
+                mbar_drain(smem_u32(&full[i % p.slots]), (uint32_t)(i / p.slots) & 1u);
         }
         __syncthreads();
         return;
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             const DistillRow<TL> r(p, i);
             const int b = i % kDtRows;
             const double dloss = kGrad ? (double)p.dloss[r.row] : 0.0;
-            mbar_wait(smem_u32(&summed_bar[b]), (uint32_t)(i / kDtRows) & 1u, abort_flag, &g_distill_status);
+            mbar_wait(smem_u32(&summed_bar[b]), (uint32_t)(i / kDtRows) & 1u, abort_flag, &g_distill_status, limit_ns);
             MaxSum s = lane < kDtWarps ? warp_part[b][lane] : MaxSum{-INFINITY, 0.f};
             if (lane >= kDtWarps && lane - kDtWarps < r.edge) {
                 const int bit = r.bit(r.edge_class(lane - kDtWarps));
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             if constexpr (kGrad) {
                 TG* dz = static_cast<TG*>(p.dlogits) + r.row * p.ld;
                 const float gT = p.temperature * p.dloss[r.row];
-                mbar_wait(smem_u32(&graded_bar[b]), (uint32_t)(i / kDtRows) & 1u, abort_flag, &g_distill_status);
+                mbar_wait(smem_u32(&graded_bar[b]), (uint32_t)(i / kDtRows) & 1u, abort_flag, &g_distill_status, limit_ns);
                 if (lane < r.edge)
                     store1(dz + r.edge_class(lane), any_of[b] ? ex2_from(edge_z[b][lane], mr_of[b], c) * factor_of[b] : 0.f);
                 __syncwarp();
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
     // number, how many groups there are, a constant where all are).
     auto through = [&](const DistillRow<TL>& r, auto&& fn) {
         for (int first = 0; first < r.groups; first += kPieceGroups) {
-            mbar_wait(smem_u32(&full[slot]), phase, abort_flag, &g_distill_status);
+            mbar_wait(smem_u32(&full[slot]), phase, abort_flag, &g_distill_status, limit_ns);
             const TL* mine = reinterpret_cast<const TL*>(smem + slot * kDtPiece) + 8 * tid;
             const int left = r.groups - first - tid;
             if (r.groups - first >= kPieceGroups) {
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
         const int b = s % kDtRows;
         const unsigned char* bytes = reinterpret_cast<const unsigned char*>(mask_of(b)) + 1;
         auto listed_yet = [&]() {
-            mbar_wait(smem_u32(&listed_bar[b]), (uint32_t)(s / kDtRows) & 1u, abort_flag, &g_distill_status);
+            mbar_wait(smem_u32(&listed_bar[b]), (uint32_t)(s / kDtRows) & 1u, abort_flag, &g_distill_status, limit_ns);
         };
         if (whole) listed_yet();
         MaxSum sum{-INFINITY, 0.f};
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
         const int b = s % kDtRows;
         TG* dz = static_cast<TG*>(p.dlogits) + r.row * p.ld;
         for (int64_t v = (int64_t)V + tid; v < p.ld; v += kSixteen) store1(dz + v, 0.f);
-        mbar_wait(smem_u32(&factors_bar[b]), (uint32_t)(s / kDtRows) & 1u, abort_flag, &g_distill_status);
+        mbar_wait(smem_u32(&factors_bar[b]), (uint32_t)(s / kDtRows) & 1u, abort_flag, &g_distill_status, limit_ns);
         const float mr = mr_of[b], from = -at(mr, c), factor = factor_of[b];
         const float2 from2 = make_float2(from, from), factor2 = make_float2(factor, factor);
         TG* out = dz + r.head;
@@ -622,14 +626,14 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
     __syncthreads();
 }
 
-template <typename TL, typename TG, bool kGrad>
-int launch(DistillArgs a, cudaStream_t stream) {
+template <typename TL, typename TG, bool kGrad, bool kTimed>
+int launch_as(DistillArgs a, cudaStream_t stream) {
     static unsigned long long init_mask = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NQ_ERR_CUDA;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(__atomic_load_n(&init_mask, __ATOMIC_ACQUIRE) & bit)) {
-        if (cudaFuncSetAttribute(distill_kernel<TL, TG, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(distill_kernel<TL, TG, kGrad, kTimed>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kDtMost) != cudaSuccess)
             return NQ_ERR_CUDA;
         __atomic_fetch_or(&init_mask, bit, __ATOMIC_RELEASE);
@@ -648,10 +652,15 @@ int launch(DistillArgs a, cudaStream_t stream) {
     // a row's second pass after the next row's first, where twice the rows stay in L2
     a.lag = kGrad && 2 * per_sm * sm_count() * row_bytes <= kDtStays;
     const int64_t at_once = (int64_t)per_sm * sm_count(), ctas = a.rows == 1 || a.tokens < at_once ? a.tokens : at_once;
-    return launch_pdl(distill_kernel<TL, TG, kGrad>, dim3((unsigned)ctas), dim3(kDtThreads),
+    return launch_pdl(distill_kernel<TL, TG, kGrad, kTimed>, dim3((unsigned)ctas), dim3(kDtThreads),
                       (size_t)a.slots * kDtPiece + a.rows * list, stream, a) == cudaSuccess
                ? NQ_OK
                : NQ_ERR_CUDA;
+}
+
+template <typename TL, typename TG, bool kGrad>
+int launch(const DistillArgs& a, cudaStream_t stream) {
+    return a.wait_ns == kWaitLimitNs ? launch_as<TL, TG, kGrad, false>(a, stream) : launch_as<TL, TG, kGrad, true>(a, stream);
 }
 
 }  // namespace
@@ -659,7 +668,8 @@ int launch(DistillArgs a, cudaStream_t stream) {
 int distill_device(const void* logits, bool logits_bf16, int64_t ld, const int32_t* ids, const float* teacher,
                    const float* teacher_lse, const float* dloss, int64_t tokens, int64_t vocab, int64_t k,
                    float temperature, float* loss, void* dlogits, bool grad_bf16, cudaStream_t stream) {
-    const DistillArgs a{logits, ld, ids, teacher, teacher_lse, dloss, loss, dlogits, (int)vocab, (int)k, temperature, tokens, 0, 0, 0};
+    const DistillArgs a{logits, ld, ids, teacher, teacher_lse, dloss, loss, dlogits, (int)vocab, (int)k, temperature, tokens, 0, 0, 0,
+                        head_wait_ns()};
     if (!dlogits)
         return logits_bf16 ? launch<uint16_t, float, false>(a, stream)
                            : launch<float, float, false>(a, stream);

@@ -177,6 +177,8 @@ int xent_forward(const uint16_t* h, const uint16_t* W, const int32_t* labels, in
 int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, const float* lse, const float* dloss,
                   int64_t tokens, int64_t vocab, int64_t d, uint16_t* dh, uint16_t* dW, void* scratch,
                   cudaStream_t stream);
+// how long the waits of these kernels last before they give up (nq_selftest_head_wait_limit)
+unsigned long long head_wait_ns();
 // read and clear the status words of these kernels (the device is idle)
 int q4_take_status(unsigned* word);
 int distill_take_status(unsigned* word);

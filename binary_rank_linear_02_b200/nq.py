@@ -108,6 +108,8 @@ def _load() -> ctypes.CDLL:
     L.nq_admm_iterate.restype = ctypes.c_int
     L.nq_admm_factorize.argtypes = [p, i64, i64, i64, p, i32, i32, f64, f64, p, p, p, p, p, p]
     L.nq_admm_factorize.restype = ctypes.c_int
+    L.nq_selftest_head_wait_limit.argtypes = [i64]
+    L.nq_selftest_head_wait_limit.restype = ctypes.c_int
     f32 = ctypes.c_float
     L.nq_pack_q4.argtypes = [p, i64, i64, p, p]
     L.nq_pack_q4.restype = i32
@@ -213,6 +215,10 @@ def device_status(stream=None) -> None:
 
 def nq_selftest_wait_timeout(limit_ns: int, stream: int = 0) -> int:
     return _lib.nq_selftest_wait_timeout(limit_ns, stream)
+
+
+def nq_selftest_head_wait_limit(limit_ns: int) -> int:
+    return _lib.nq_selftest_head_wait_limit(limit_ns)
 
 
 def nq_version() -> int:

@@ -549,6 +549,15 @@ int nq_device_status(void* stream);
  */
 int nq_selftest_wait_timeout(int64_t limit_ns, void* stream);
 
+/*
+ * nq_selftest_head_wait_limit -- the waits in the output head's kernels give up after 2 s of GPU
+ * time; those of calls made after this one do after `limit_ns` (0: 2 s again).  With a limit shorter
+ * than what is waited for, a call ends early: its results are not to be used, nq_device_status
+ * returns NQ_ERR_TIMEOUT (and clears it), and the device stays usable.  For the whole process.
+ * 0 <= limit_ns <= 1e10, else NQ_ERR_VALUE.
+ */
+int nq_selftest_head_wait_limit(int64_t limit_ns);
+
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int nq_version(void);
 

@@ -1,0 +1,48 @@
+"""Waits of the output head's kernels that give up: the call ends, with the copies that it has in
+flight landed, the status is reported once, and the same call is right afterwards.
+
+The limit is a microsecond of GPU time, and the work that is waited for is far longer than that.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from binary_rank_linear_02_b200 import nq as mod
+
+    return mod
+
+
+def gives_up_and_recovers(nq, call):
+    want = call()
+    nq.device_status()
+    stream = torch.cuda.current_stream().cuda_stream
+    for _ in range(3):
+        assert nq.nq_selftest_head_wait_limit(1000) == nq.NQ_OK
+        try:
+            call()
+        finally:
+            assert nq.nq_selftest_head_wait_limit(0) == nq.NQ_OK
+        assert nq.nq_device_status(stream) == nq.NQ_ERR_TIMEOUT
+        assert nq.nq_device_status(stream) == nq.NQ_OK
+        for a, b in zip(want, call()):
+            assert torch.equal(a, b)
+        nq.device_status()
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("tokens,vocab", [(3, 1 << 20), (500, 200001)])
+def test_distill_gives_up(nq, tokens, vocab, rest):
+    g = torch.Generator(device="cuda").manual_seed(11)
+    logits = torch.randn(tokens, vocab, device="cuda", generator=g)
+    ids = torch.randint(0, vocab, (tokens, 7), device="cuda", generator=g, dtype=torch.int32)
+    teacher = torch.randn(tokens, 7, device="cuda", generator=g)
+    lse = torch.full((tokens,), 4.0, device="cuda") if rest else None
+    dloss = torch.ones(tokens, device="cuda")
+    gives_up_and_recovers(nq, lambda: (nq.distill_topk_fwd(logits, ids, teacher, vocab, teacher_lse=lse),))
+    gives_up_and_recovers(nq, lambda: nq.distill_topk_bwd(logits, ids, teacher, vocab, dloss, teacher_lse=lse))

@@ -36,3 +36,10 @@ def test_distill_temperature_range(nq, ptrs):
         assert both(t) == nq.NQ_ERR_VALUE
     for t in (tiny, 1e-30, 1e30, huge):
         assert both(t) == nq.NQ_ERR_PTRKIND
+
+
+def test_head_wait_limit_range(nq):
+    for bad in (-1, 10**10 + 1):
+        assert nq.nq_selftest_head_wait_limit(bad) == nq.NQ_ERR_VALUE
+    for good in (1, 10**10, 0):  # (0, the last one, is the usual limit)
+        assert nq.nq_selftest_head_wait_limit(good) == nq.NQ_OK
