@@ -142,6 +142,7 @@ struct Q4Args {
     int scale_copy;          // bytes of a copy of scales: 16, 8 or 4 (2: rows of an odd number of them, in fours)
     int scale_pitch;         // bytes between rows of a stage's scales
     int panel;               // columns whose x is in shared memory at a time (all, or a multiple of 2048)
+    unsigned long long wait_ns;  // how long a wait lasts
 };
 
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int width) {
@@ -237,7 +238,9 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
             for (int set = 0; set < sets && ok; ++set) {
                 const int row = (int)(blockIdx.x + set * gridDim.x) * set_rows;
                 for (int k = 0; k < per_set; ++k, ++it) {
-                    ok = mbar_wait(smem_u32(&empty[st]), phase ^ 1u, abort_flag, &g_q4_status);
+                    // the stage is free, and (a lane sees to it) what was last fetched into it has landed: a
+                    // warp that gave up frees stages without having waited for them
+                    ok = mbar_wait(smem_u32(lane == 31 ? &full[st] : &empty[st]), phase ^ 1u, abort_flag, &g_q4_status, p.wait_ns);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
@@ -274,9 +277,9 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
                 }
             }
         }
-        // given up: what is in flight lands before the CTA leaves
+        // whoever gave up, if any: what is in flight lands before the CTA leaves
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok && lane == 0)
+        if (lane == 0)
             for (int i = it < p.stages ? 0 : it - p.stages; i < it; ++i)
                 mbar_drain(smem_u32(&full[i % p.stages]), (uint32_t)(i / p.stages) & 1u);
         __syncthreads();
@@ -303,7 +306,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
     auto add_up = [&](int no) {
         const int buf = no % kQParts, panel = no / sets, set = no - panel * sets;
         if (warp / kQAdders != set % (kQWarps / kQAdders)) return;  // (a set's sums are the same threads' in all panels)
-        mbar_wait(smem_u32(&written[buf]), (uint32_t)(no / kQParts) & 1u, abort_flag, &g_q4_status);
+        mbar_wait(smem_u32(&written[buf]), (uint32_t)(no / kQParts) & 1u, abort_flag, &g_q4_status, p.wait_ns);
         for (int e = threadIdx.x % (32 * kQAdders); e < p.tps * 16 * kQTokens; e += 32 * kQAdders) {
             const int r = e & 15, b = e / 16 % kQTokens, tile = e / (16 * kQTokens);
             float sum = 0.f;
@@ -388,7 +391,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
             int k = first;
             for (; k < per_set; k += 2) {
                 // (a wait that gives up is recorded and ends the others: the CTA runs out in bounded time)
-                mbar_wait(smem_u32(&full[st]), phase, abort_flag, &g_q4_status);
+                mbar_wait(smem_u32(&full[st]), phase, abort_flag, &g_q4_status, p.wait_ns);
                 const int at_block = k * p.blocks + block;
                 const uint32_t at0 = frag + (uint32_t)(st * kQCodeBytes), h_at0 = scale_at + (uint32_t)st * scale_stage;
                 const unsigned char* xat0 = xrow + 2 * kQCols * at_block;
@@ -450,7 +453,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
             }
             first = k - per_set;
             // the warps' shares of the set's tiles
-            if (no >= kQParts) mbar_wait(smem_u32(&added[no % kQParts]), (uint32_t)(no / kQParts - 1) & 1u, abort_flag, &g_q4_status);
+            if (no >= kQParts) mbar_wait(smem_u32(&added[no % kQParts]), (uint32_t)(no / kQParts - 1) & 1u, abort_flag, &g_q4_status, p.wait_ns);
             float(&mine)[16][kQTokens] = part[no % kQParts][warp];
             *reinterpret_cast<float2*>(&mine[g][2 * t]) = make_float2(out[0], out[1]);
             *reinterpret_cast<float2*>(&mine[g + 8][2 * t]) = make_float2(out[2], out[3]);
@@ -568,7 +571,7 @@ int q4_zeros(const Q4Args& p, const uint32_t* W, cudaStream_t stream) {
 
 int q4_forward(const uint16_t* x, const uint32_t* W, const uint16_t* scales, const uint16_t* zeros, int64_t m,
                int64_t n, int group, int64_t batch, float* y, cudaStream_t stream) {
-    const Q4Args p{x, scales, zeros, y, m, n, batch, 0, 0, 0, 0, 0, 0};
+    const Q4Args p{x, scales, zeros, y, m, n, batch, 0, 0, 0, 0, 0, 0, head_wait_ns()};
     return group == 32   ? q4_zeros<32>(p, W, stream)
            : group == 64 ? q4_zeros<64>(p, W, stream)
                          : q4_zeros<128>(p, W, stream);

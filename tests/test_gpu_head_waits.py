@@ -46,3 +46,38 @@ def test_distill_gives_up(nq, tokens, vocab, rest):
     dloss = torch.ones(tokens, device="cuda")
     gives_up_and_recovers(nq, lambda: (nq.distill_topk_fwd(logits, ids, teacher, vocab, teacher_lse=lse),))
     gives_up_and_recovers(nq, lambda: nq.distill_topk_bwd(logits, ids, teacher, vocab, dloss, teacher_lse=lse))
+
+
+
+def test_q4_gives_up(nq):
+    """The kernel's own waits are a few microseconds long; here x lies in managed memory that the host
+    has just written, so that its pages come over first, while the fetching warp waits."""
+    import ctypes
+
+    import numpy as np
+
+    m, n, group, batch = 100, 1 << 20, 128, 8
+    g = torch.Generator(device="cuda").manual_seed(12)
+    w = torch.randint(-(1 << 31), 1 << 31, (m, n // 8), device="cuda", generator=g, dtype=torch.int32)
+    scales, zeros = (torch.rand(m, n // group, device="cuda", generator=g).half() for _ in range(2))
+    x = torch.randn(batch, n, device="cuda", generator=g).bfloat16()
+    bits = x.view(torch.int16).cpu().numpy()
+    runtime = ctypes.CDLL("libcudart.so.12")
+    at = ctypes.c_void_p()
+    assert runtime.cudaMallocManaged(ctypes.byref(at), ctypes.c_size_t(bits.nbytes), ctypes.c_uint(1)) == 0
+    try:
+        there = np.ctypeslib.as_array(ctypes.cast(at, ctypes.POINTER(ctypes.c_int16)), bits.shape)
+
+        def call():
+            there[:] = bits
+            y = torch.empty(batch, m, device="cuda")
+            assert nq.lib().nq_q4_linear_fwd(at.value, w.data_ptr(), scales.data_ptr(), zeros.data_ptr(), m, n, group,
+                                             batch, y.data_ptr(), torch.cuda.current_stream().cuda_stream) == nq.NQ_OK
+            torch.cuda.synchronize()
+            return (y,)
+
+        assert torch.equal(call()[0], nq.q4_linear_fwd(x, w, scales, m, n, group, zeros=zeros))
+        gives_up_and_recovers(nq, call)
+    finally:
+        torch.cuda.synchronize()
+        runtime.cudaFree(at)
