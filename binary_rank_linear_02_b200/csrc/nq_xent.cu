@@ -81,6 +81,7 @@ struct XentBarriers {
     unsigned long long acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
+    int issued[2], taken;  // K blocks that the pair's CTAs have loads of, and that the MMAs were given (in both CTAs)
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -88,11 +89,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
     return r;
 }
-// The address of this CTA's shared-memory location in the cluster's first CTA.
-__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+// The address of this CTA's shared-memory location in the cluster's CTA `rank`, and in its first one.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
+}
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return in_cta(addr, 0); }
+__device__ __forceinline__ void store_in_both(int* p, int v) {
+    for (uint32_t rank = 0; rank < 2; ++rank)
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(in_cta(smem_u32(p), rank)), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
@@ -401,7 +407,23 @@ struct XentPlan {
                      // of A's K blocks begins (both 0: no such halves)
     int part;        // K blocks that are summed in tensor memory before the epilogue takes them
     int n_fastest;  // the order of the tiles: neighbours in the first index run at the same time
+    unsigned long long wait_ns;  // how long a wait lasts
 };
+
+// Waits (the first CTA) for the loads of the pair that no MMA waited for, all of which report to the
+// first CTA's barriers: to each at most one use that is not complete.  Where only one of the CTAs
+// loads a block, the other's bytes, or the first one's announcement, are made up for.
+__device__ __noinline__ void xent_land(XentBarriers& bar, int stages, uint32_t stage_bytes) {
+    const int both = bar.issued[0] < bar.issued[1] ? bar.issued[0] : bar.issued[1];
+    const int last = bar.issued[0] + bar.issued[1] - both;
+    for (int i = bar.taken; i < last; ++i) {
+        const uint32_t full = smem_u32(&bar.full[i % stages]);
+        if (i >= both && bar.issued[0] == both) mbar_expect_tx(full, stage_bytes);
+        if (i >= both && bar.issued[1] == both)
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full), "r"(stage_bytes) : "memory");
+        mbar_drain(full, (uint32_t)(i / stages) & 1u);
+    }
+}
 
 // A persistent pair of CTAs per two SMs walks over the tiles.  Warp 0 loads (each CTA its own
 // halves of A and B, reporting to the first CTA's barriers), warp 1 of the first CTA issues the
@@ -436,7 +458,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
             mbar_init(smem_u32(&bar.acc_empty[i]), 2 * kXEpilogueWarps);  // of both CTAs
         }
         mbar_init(smem_u32(&bar.drain), 1);
-        bar.abort_flag = 0;
+        bar.abort_flag = bar.issued[0] = bar.issued[1] = bar.taken = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -478,7 +500,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                 tile_of(item, tm, tn, kb0, kb1);
                 const int m0 = tm * kXTile + (int)rank * kXHalfTile, n0 = tn * plan.bn + (int)rank * half_bn;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    if (!mbar_wait(smem_u32(&bar.empty[st]), ph ^ 1u, abort_flag, status)) {
+                    if (!mbar_wait(smem_u32(&bar.empty[st]), ph ^ 1u, abort_flag, status, plan.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -508,14 +530,11 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                     }
                 }
             }
-            // given up: what the pair has in flight reports to the first CTA's barriers
-            if (!ok && rank == 0)
-                for (int i = it < stages ? 0 : it - stages; i < it; ++i)
-                    mbar_drain(smem_u32(&bar.full[i % stages]), (uint32_t)(i / stages) & 1u);
+            store_in_both(&bar.issued[rank], it);
         }
         if (warp == 1 && lane == 0 && rank == 0) {
             const uint32_t idesc = xent_idesc(AMN, BMN, plan.bn);
-            int n = 0, st = 0;
+            int n = 0, st = 0, taken = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int item = pair; item < items && ok; item += pairs) {
@@ -524,7 +543,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                 for (int p0 = kb0; p0 < kb1 && ok; p0 += plan.part, ++n) {
                     const int p1 = p0 + plan.part < kb1 ? p0 + plan.part : kb1;
                     const int acc = n & 1;
-                    if (!mbar_wait(smem_u32(&bar.acc_empty[acc]), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, status)) {
+                    if (!mbar_wait(smem_u32(&bar.acc_empty[acc]), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, status, plan.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -534,7 +553,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                         const uint32_t d = kT ? d0 + (uint32_t)(turn * plan.bn) : d0;
                         const int before = kT ? plan.accs : 1;  // K blocks that begin an accumulator
                         if (kT && ++turn == plan.accs) turn = 0;
-                        if (!mbar_wait(smem_u32(&bar.full[st]), ph, abort_flag, status)) {
+                        if (!mbar_wait(smem_u32(&bar.full[st]), ph, abort_flag, status, plan.wait_ns)) {
                             ok = false;
                             break;
                         }
@@ -548,6 +567,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                             pair_mma(d, ad + (uint64_t)k * astep, bd + (uint64_t)k * bstep, idesc,
                                      (kb >= p0 + before || k > 0) ? 1u : 0u);
                         pair_commit(smem_u32(&bar.empty[st]));
+                        ++taken;
                         if (++st == stages) {
                             st = 0;
                             ph ^= 1u;
@@ -556,10 +576,10 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                     if (ok) pair_commit(smem_u32(&bar.acc_full[acc]));
                 }
             }
-            if (!ok) {
-                pair_commit(smem_u32(&bar.drain));
-                mbar_drain(smem_u32(&bar.drain), 0);
-            }
+            // whoever gave up, if any: the MMAs are done with both CTAs' memory before either leaves
+            store_in_both(&bar.taken, taken);
+            pair_commit(smem_u32(&bar.drain));
+            mbar_drain(smem_u32(&bar.drain), 0);
         }
     } else {
         if constexpr (kKeeps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kXManyRegs));
@@ -583,7 +603,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
             for (int p0 = kb0; p0 < kb1 && ok; p0 += plan.part, ++n) {
                 const int acc = n & 1;
                 // (the warp goes on, or gives up, as one)
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar.acc_full[acc]), (uint32_t)(n >> 1) & 1u, abort_flag, status));
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar.acc_full[acc]), (uint32_t)(n >> 1) & 1u, abort_flag, status, plan.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t taddr = tmem + lanes + (uint32_t)(acc * kXTile);
@@ -636,6 +656,12 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may still signal it
+    if (bar.issued[0] != bar.taken || bar.issued[1] != bar.taken) {  // somewhere a wait gave up
+        if (threadIdx.x == 0 && cluster_rank() == 0) xent_land(bar, plan.stages, kXABytes + 64u * (uint32_t)plan.bn);
+        __syncthreads();
+        cluster_sync();
+    }
+    if (threadIdx.x == 32 && rank == 1) mbar_drain(smem_u32(&bar.drain), 0);  // (the last of the MMAs' signals to this CTA)
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
@@ -755,6 +781,7 @@ int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, 
     plan.part = kEpi == kStats && !kT && parts > 1 ? (int)cut(plan.nkb, parts) : plan.per_split;
     plan.splits = splits;
     plan.n_fastest = n_fastest;
+    plan.wait_ns = head_wait_ns();
     const int64_t items = (int64_t)plan.tm * plan.tn * splits, pairs = sm_count() / 2;
     return launch_pdl(xent_gemm_kernel<kEpi, AMN, BMN, kT>, dim3((unsigned)(2 * (items < pairs ? items : pairs))),
                       dim3(kXThreads), (size_t)kXSmem, stream, amap, bmap, plan, e) == cudaSuccess
