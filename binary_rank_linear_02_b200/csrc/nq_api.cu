@@ -834,16 +834,17 @@ int nq_device_status(void* stream) {
     if (!ws) return st;
     unsigned word = 0;
     if (cudaMemcpy(&word, ws->status + 1, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess) return NQ_ERR_CUDA;
-    if (word != 0 && cudaMemset(ws->status + 1, 0, sizeof(unsigned)) != cudaSuccess) return NQ_ERR_CUDA;
-    // the kernels of the output head have words of their own
+    // a kernel that gave up may have left arrival counters part-way: start them from zero again
+    if (word != 0 && (cudaMemset(ws->status + 1, 0, sizeof(unsigned)) != cudaSuccess ||
+                      cudaMemset(ws->counters, 0, sizeof(int) * (ws->counter_cap + 1)) != cudaSuccess))
+        return NQ_ERR_CUDA;
+    // the kernels of the output head have words of their own, and no counters: the workspace may be in
+    // use on another stream
     for (auto take : {q4_take_status, distill_take_status, xent_take_status}) {
         unsigned head = 0;
         if (take(&head) != NQ_OK) return NQ_ERR_CUDA;
         if (word == 0) word = head;
     }
-    // a kernel that gave up may have left arrival counters part-way: start them from zero again
-    if (word != 0 && cudaMemset(ws->counters, 0, sizeof(int) * (ws->counter_cap + 1)) != cudaSuccess)
-        return NQ_ERR_CUDA;
     return word == 0 ? NQ_OK : -(int)word;
 }
 

@@ -96,3 +96,41 @@ def test_cross_entropy_gives_up(nq, tokens, vocab, d):
     gives_up_and_recovers(nq, lambda: nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss))
     # (above 256 tokens the forward's sums are taken in parts, whose waits may be too short to give up)
     gives_up_and_recovers(nq, lambda: nq.linear_cross_entropy_fwd(h, W, labels), always=tokens <= 256)
+
+
+def test_head_status_leaves_the_workspace_alone(nq):
+    """The head shares no workspace: reading and clearing the status of a call that gave up does not
+    reach into the arrival counters of the factorised layers' calls under way on another stream."""
+    import numpy as np
+
+    from binary_rank_linear_02_b200 import synth
+
+    m, n, r = 4096, 4096, 1024
+    dev = torch.device("cuda")
+    Us, Vs = synth.signs(m, r, 3, "U"), synth.signs(n, r, 3, "V")
+    Upk = nq.pack_signs(torch.from_numpy(Us).to(dev))
+    Vpk = nq.pack_signs(torch.from_numpy(np.ascontiguousarray(Vs.T)).to(dev))
+    s1 = torch.from_numpy(synth.scales_f16(m, 3, "s1").view(np.int16)).to(dev)
+    s2 = torch.from_numpy(synth.scales_f16(n, 3, "s2").view(np.int16)).to(dev)
+    xs = [torch.from_numpy(synth.activations_bf16(b, n, 3).view(np.int16)).to(dev) for b in (1, 5, 40)]
+    want = [nq.lowrank_linear_fwd(x, Upk, Vpk, s1, s2, m, n, r) for x in xs]
+    vocab = 1 << 20
+    logits = torch.zeros(3, vocab, device="cuda")
+    ids, teacher = torch.zeros(3, 1, dtype=torch.int32, device="cuda"), torch.zeros(3, 1, device="cuda")
+    loss = torch.empty(3, device="cuda")
+    head, layers = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    try:
+        for _ in range(10):
+            assert nq.nq_selftest_head_wait_limit(1000) == nq.NQ_OK
+            nq.distill_topk_fwd(logits, ids, teacher, vocab, loss=loss, stream=head.cuda_stream)
+            with torch.cuda.stream(layers):
+                got = [[nq.lowrank_linear_fwd(x, Upk, Vpk, s1, s2, m, n, r) for x in xs] for _ in range(20)]
+            assert nq.nq_device_status(head.cuda_stream) == nq.NQ_ERR_TIMEOUT
+            torch.cuda.synchronize()
+            assert nq.nq_device_status(0) == nq.NQ_OK
+            for y in got:
+                for a, b in zip(want, y):
+                    assert torch.equal(a, b)
+    finally:
+        nq.nq_selftest_head_wait_limit(0)
