@@ -89,6 +89,8 @@ __device__ __forceinline__ float high_half(uint32_t v) { return __half2float(__u
 __device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
+__device__ __forceinline__ float sum_bf16(uint32_t v) { return fmaf(high_bf16(v), 0x1p-16f, low_bf16(v) * 0x1p-16f); }  // 2^-16 of it
+
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -323,7 +325,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
                 *kp = sum;
             }
             const int64_t row = ((int64_t)blockIdx.x + (int64_t)set * gridDim.x) * set_rows + 16 * tile + r;
-            if (panel == panels - 1 && row < p.m && b < ntok) p.y[(tok0 + b) * p.m + row] = 256.f * sum;
+            if (panel == panels - 1 && row < p.m && b < ntok) p.y[(tok0 + b) * p.m + row] = 65536.f * sum;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&added[buf]));
@@ -337,7 +339,8 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
         if (panel > 0) asm volatile("barrier.sync 1, %0;" ::"n"(32 * kQWarps) : "memory");  // the place of x is free again
         // x, 8 columns a lane; a tree over a group's lanes gives its largest value and its sum.  A
         // group's values are multiplied by 2^shift; what undoes it (and 2^-133) is kept as
-        // 2^(125 - shift), 2^-8 of it, and so is 2^-8 of the sum.
+        // 2^(117 - shift), 2^-16 of it, and so is 2^-16 of the sum: a group's sums of the largest
+        // bfloat16 numbers, 15 times them and more, stay finite (and 2^-16 of the smallest is exact).
         const int units = width / 8;  // a multiple of 16, a group of its divisors
         constexpr int kBatch = 8;
         int next_tok = 0, next_unit = warp * 32 + lane;
@@ -363,8 +366,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
                 const uint32_t top2 = max_bf16x2(max_bf16x2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
                                                  max_bf16x2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
                 uint32_t top = max(top2 >> 16, top2 & 0xFFFFu);
-                float s = ((low_bf16(v[i].x) + high_bf16(v[i].x)) + (low_bf16(v[i].y) + high_bf16(v[i].y))) +
-                          ((low_bf16(v[i].z) + high_bf16(v[i].z)) + (low_bf16(v[i].w) + high_bf16(v[i].w)));
+                float s = (sum_bf16(v[i].x) + sum_bf16(v[i].y)) + (sum_bf16(v[i].z) + sum_bf16(v[i].w));
 #pragma unroll
                 for (int o = 1; o < kGroup / 8; o <<= 1) {
                     s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -380,7 +382,7 @@ q4_kernel(const __grid_constant__ CUtensorMap wmap, const Q4Args p) {
                                    mul_bf16x2(__byte_perm(v[i].y, v[i].w, 0x7632), f1));
                     if (unit[i] % (kGroup / 8) == 0)
                         reinterpret_cast<float2*>(sums + unit[i] / (kGroup / 8) * pairs)[tok[i]] =
-                            make_float2(__uint_as_float((uint32_t)(252 - shift) << 23), s * (kZeros ? 0x1p-8f : 0x1p-5f));
+                            make_float2(__uint_as_float((uint32_t)(244 - shift) << 23), s * (kZeros ? 1.f : 8.f));
                 }
             }
         }

@@ -382,9 +382,14 @@ int nq_pack_q4(const uint8_t* codes, int64_t rows, int64_t cols, uint32_t* out, 
  *            m, n at most 1<<20
  *   batch  : 0 (a no-op) to 524280 (else NQ_ERR_BATCH).  Made for the few tokens of a decode
  *            step: up to 8 tokens read the codes once, more read them again for every 8.
- * Products are exact and sums are fp32: |error| <= (48 + n/32) 2^-23 sum_j |s| (c + |z|) |x_j|.
- * Each token's result does not depend on the others; an infinity or a NaN in a token's x makes
- * that token's results NaN or infinite.
+ * Products are exact and sums are fp32: |error| <= (48 + n/32) 2^-23 sum_j |s| (c + |z|) |x_j|, of
+ * finite x of any size as long as (c + |z|) |x_j| adds up to less than 2^143 within each group (it
+ * does for |z| <= 240), |s| times it over all groups too, and y is finite; below 2^-100, y is rounded
+ * to multiples of 2^-133.
+ * No token's values reach another token's result; an infinity or a NaN in a token's x makes that
+ * token's results NaN or infinite.  The order of a sum over n goes by m, n, group and batch (columns
+ * are taken in panels where x of all tokens is too much for shared memory), so that the same token
+ * may differ in the last bits between calls of other batch sizes.
  */
 int nq_q4_linear_fwd(const void* x, const uint32_t* Wq, const void* scales, const void* zeros, int64_t m, int64_t n,
                      int64_t group, int64_t batch, float* y, void* stream);
