@@ -447,12 +447,18 @@ int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const i
  *             (scratch_bytes smaller: NQ_ERR_NOMEM), free again when the call's work is done
  *   tokens : 0 .. 1<<24 (else NQ_ERR_BATCH; with 0, bwd writes dW with zeros);  vocab : 1 ..
  *   1<<20;  d : a positive multiple of 8, at most 1<<20 (else NQ_ERR_SHAPE).
- * Forward: products exact, sums fp32.  Backward: dz passes through bfloat16 (the operand type
- * of the tensor cores beside h and W), sums over classes and tokens are fp32, results are
- * rounded once to bfloat16: |error of dh_ij| <= 2^-8 (sum_v |dz_iv W_vj| + |dh_ij|), likewise
- * dW.  Up to 128 tokens dz is two bfloat16 parts: 2^-16 in place of the first 2^-8.  The scratch of bwd is bounded: dz exists for a piece of the vocabulary at a time (at
- * most 256 MB, or 256 classes), and dh's sums in fp32 in shares (at most 256 MB, or 4 tokens d
- * bytes).  Repeated calls agree bit for bit.
+ * Forward: products exact, sums fp32: a logit is off by at most ez = (d/16 + 16) 2^-23 sum_j |h_ij W_vj|,
+ * lse by the largest ez of its row and (vocab/32 + 64 + |lse|) 2^-23, loss by twice that and its label's
+ * part of it.  Backward: z is computed again, p = exp(z - lse) in fp32 from the lse that is given; dz passes
+ * through bfloat16 (the operand type of the tensor cores beside h and W), up to 128 tokens as two
+ * bfloat16 parts; sums over classes and tokens are fp32; results are rounded once to bfloat16.  With
+ * r = 2^-8, or 2^-16 up to 128 tokens,
+ *     |error of dz_iv| <= r |dz_iv| + |dloss_i| (p_iv (2 ez + 2^-18) + 2^-23) =: edz,
+ *     |error of dh_ij| <= sum_v edz_iv |W_vj| + (vocab/8 + 32) 2^-23 sum_v |dz_iv W_vj| + 2^-8 |dh_ij|,
+ * the last two up to a factor of 1 + 2^-6, likewise dW with sums over the tokens.  (The 2^-23 counts
+ * where p is 1 but for less than that: a token that is sure of its label.)  The scratch of bwd is
+ * bounded: dz exists for a piece of the vocabulary at a time (at most 256 MB, or 256 classes), and dh's
+ * sums in fp32 in shares (at most 256 MB, or 4 tokens d bytes).  Repeated calls agree bit for bit.
  */
 int64_t nq_linear_cross_entropy_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d, int backward);
 int nq_linear_cross_entropy_fwd(const void* h, const void* W, const int32_t* labels, int64_t tokens, int64_t vocab,

@@ -45,3 +45,102 @@ def test_q4_activations_of_any_size(nq, size, group, zeros):
     mag = x.double().abs() @ ((c + zz) * s).T
     assert torch.all(ref.abs() < 3e38)
     assert torch.all((y.double() - ref).abs() <= (48 + n / 32) * U * mag + n / 32 * 27 * 2.0 ** -134 * 4.0)
+
+
+@pytest.mark.parametrize("tokens", [5, 128, 129, 400])
+@pytest.mark.parametrize("gap", [3.0, 9.0, 14.0, 30.0])
+def test_cross_entropy_gradients_of_sure_tokens(nq, tokens, gap):
+    """Tokens whose label's logit is `gap` above what the others add up to, so that p - 1 is a small
+    difference: the gradients are within the bound that the header states (which is checked as
+    stated, with p from the lse that the forward gave), and so are those of hopeless tokens."""
+    vocab, d = 500, 256
+    g = torch.Generator(device="cuda").manual_seed(31)
+    W = (torch.randn(vocab, d, device="cuda", generator=g) / 16).bfloat16()
+    labels = torch.randint(0, vocab, (tokens,), device="cuda", generator=g, dtype=torch.int32)
+    h = (W[labels.long()].float() * gap * 2 + torch.randn(tokens, d, device="cuda", generator=g) * 0.3).bfloat16()
+    labels[1::4] = (labels[1::4] + 1) % vocab  # hopeless
+    dloss = torch.rand(tokens, device="cuda", generator=g) + 0.1
+    _, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    dh, dW = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    hd, Wd, dl = h.double(), W.double(), dloss.double()[:, None]
+    z = hd @ Wd.T
+    ez = (d / 16 + 16) * U * (hd.abs() @ Wd.abs().T)
+    p = torch.exp(z - lse.double()[:, None])
+    dz = p * dl
+    dz[torch.arange(tokens, device="cuda"), labels.long()] -= dl[:, 0]
+    r = 2.0 ** -16 if tokens <= 128 else 2.0 ** -8
+    edz = r * dz.abs() + dl * (p * (2 * ez + 2.0 ** -18) + 2.0 ** -23)
+    for got, e, x, b, terms in ((dh, edz, dz, Wd, vocab), (dW, edz.T, dz.T, hd, tokens)):
+        ref = x @ b
+        bound = e @ b.abs() + (terms / 8 + 32) * U * (x.abs() @ b.abs()) + BF * ref.abs()
+        assert torch.all((got.double() - ref).abs() <= bound * (1 + 2.0 ** -6) + 1e-38)
+
+
+def test_cross_entropy_head_past_four_gigabytes(nq):
+    """A head, and its gradient, of more than 2^32 bytes: classes at both ends."""
+    tokens, vocab, d = 20, 1 << 20, 2056
+    g = torch.Generator(device="cuda").manual_seed(32)
+    W = torch.empty(vocab, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g) * (1.0 / 64)
+    h = torch.randn(tokens, d, device="cuda", generator=g).bfloat16()
+    labels = torch.tensor([0, 1, vocab - 1, vocab - 2, vocab // 2, -100] + [vocab - 3] * 14, device="cuda", dtype=torch.int32)
+    dloss = torch.rand(tokens, device="cuda", generator=g) + 0.1
+    loss, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    dh, dW = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    hd, dl = h.double(), torch.where(labels >= 0, dloss, 0.0).double()[:, None]
+    total = torch.zeros(tokens, dtype=torch.float64, device="cuda")
+    want = torch.zeros(tokens, d, dtype=torch.float64, device="cuda")
+    slack = torch.zeros_like(want)
+    worst = torch.zeros(tokens, dtype=torch.float64, device="cuda")
+    for v0 in range(0, vocab, 1 << 16):
+        Wd = W[v0:v0 + (1 << 16)].double()
+        z = hd @ Wd.T
+        total += z.exp().sum(1)
+        ez = (d / 16 + 16) * U * (hd.abs() @ Wd.abs().T)
+        worst = torch.maximum(worst, ez.amax(1))
+        p = torch.exp(z - lse.double()[:, None])
+        dz = p * dl
+        for i, v in enumerate(labels.tolist()):
+            if v0 <= v < v0 + (1 << 16):
+                dz[i, v - v0] -= dl[i, 0]
+        edz = 2.0 ** -16 * dz.abs() + dl * (p * (2 * ez + 2.0 ** -18) + 2.0 ** -23 * (dz < 0))
+        want += dz @ Wd
+        slack += edz @ Wd.abs() + (vocab / 8 + 32) * U * (dz.abs() @ Wd.abs())
+        if v0 in (0, vocab // 2, vocab - (1 << 16)):
+            ref = dz.T @ hd
+            bound = edz.T @ hd.abs() + (tokens / 8 + 32) * U * (dz.T.abs() @ hd.abs()) + BF * ref.abs()
+            assert torch.all((dW[v0:v0 + (1 << 16)].double() - ref).abs() <= bound * (1 + 2.0 ** -6) + 1e-38)
+    ref = total.log()
+    assert torch.all((lse.double() - ref).abs() <= worst + (vocab / 32 + 64 + ref.abs()) * U)
+    assert torch.all((dh.double() - want).abs() <= (slack + BF * want.abs()) * (1 + 2.0 ** -6) + 1e-38)
+
+
+def test_cross_entropy_tokens_past_four_gigabytes(nq):
+    """Hidden states, and their gradient, of more than 2^32 bytes: tokens at both ends."""
+    tokens, vocab, d = 270000, 300, 8200
+    g = torch.Generator(device="cuda").manual_seed(33)
+    h = torch.empty(tokens, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    W = (torch.randn(vocab, d, device="cuda", generator=g) / 64).bfloat16()
+    labels = torch.randint(-1, vocab, (tokens,), device="cuda", generator=g, dtype=torch.int32)
+    dloss = torch.rand(tokens, device="cuda", generator=g) + 0.1
+    loss, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    dh, _ = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss, need_dW=False)
+    Wd = W.double()
+    for at in (0, 131000, 261860, tokens - 300):  # (2^31 elements are passed in row 261888)
+        rows = slice(at, at + 300)
+        hd, counted = h[rows].double(), labels[rows] >= 0
+        dl = torch.where(counted, dloss[rows], 0.0).double()[:, None]
+        z = hd @ Wd.T
+        ez = (d / 16 + 16) * U * (hd.abs() @ Wd.abs().T)
+        ref = torch.logsumexp(z, 1)
+        off = ez.amax(1) + (vocab / 32 + 64 + ref.abs()) * U
+        assert torch.all((lse[rows].double() - ref).abs() <= off)
+        picked = z.gather(1, labels[rows].clamp_min(0).long()[:, None])[:, 0]
+        want = torch.where(counted, ref - picked, 0.0)
+        assert torch.all((loss[rows].double() - want).abs() <= 2 * off + U * picked.abs())
+        p = torch.exp(z - lse[rows].double()[:, None])
+        dz = p * dl
+        dz[torch.arange(300, device="cuda")[counted], labels[rows][counted].long()] -= dl[counted, 0]
+        edz = 2.0 ** -8 * dz.abs() + dl * (p * (2 * ez + 2.0 ** -18) + 2.0 ** -23)
+        ref = dz @ Wd
+        bound = edz @ Wd.abs() + (vocab / 8 + 32) * U * (dz.abs() @ Wd.abs()) + BF * ref.abs()
+        assert torch.all((dh[rows].double() - ref).abs() <= bound * (1 + 2.0 ** -6) + 1e-38)
