@@ -212,8 +212,8 @@ template <typename TL, typename TG, bool kGrad, bool kTimed>
 __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArgs p) {
     const unsigned long long limit_ns = kTimed ? p.wait_ns : kWaitLimitNs;
     constexpr int kGroupBytes = 8 * sizeof(TL), kPieceGroups = kDtPiece / kGroupBytes;
-    constexpr int kSixteen = 32 * kDtWarps;               // threads that go through the rows
-    constexpr int kPerThread = kPieceGroups / kSixteen;   // groups of 8 classes a thread has of a piece
+    constexpr int kRowThreads = 32 * kDtWarps;               // threads that go through the rows
+    constexpr int kPerThread = kPieceGroups / kRowThreads;   // groups of 8 classes a thread has of a piece
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ MaxSum warp_part[kDtRows][kDtWarps];
     __shared__ unsigned long long full[kDtMaxSlots], empty[kDtMaxSlots];
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                 if (sid[k] >= 0) mask[r.bit(sid[k]) >> 5] = 0;
             __syncwarp();
         };
-        // The row after next's list is read while the sixteen are in the rows before it.
+        // The row after next's list is read while the eight are in the rows before it.
         read_list(0);
         if (n > 1) read_list(1);
         for (int i = 0; i < n; ++i) {
@@ -499,10 +499,10 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             if (r.groups - first >= kPieceGroups) {
 #pragma unroll
                 for (int q = 0; q < kPerThread; q += 2)
-                    fn(mine + 8 * q * kSixteen, first + tid + q * kSixteen, std::integral_constant<int, 2>());
+                    fn(mine + 8 * q * kRowThreads, first + tid + q * kRowThreads, std::integral_constant<int, 2>());
             } else
-                for (int q = 0; q < kPerThread && q * kSixteen < left; ++q)
-                    fn(mine + 8 * q * kSixteen, first + tid + q * kSixteen, std::integral_constant<int, 1>());
+                for (int q = 0; q < kPerThread && q * kRowThreads < left; ++q)
+                    fn(mine + 8 * q * kRowThreads, first + tid + q * kRowThreads, std::integral_constant<int, 1>());
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
             if (++slot == p.slots) {
@@ -525,11 +525,11 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             constexpr int kCount = decltype(count)::value;
             float2 v[kCount][4];
 #pragma unroll
-            for (int q = 0; q < kCount; ++q) load8(at8 + 8 * q * kSixteen, v[q]);
+            for (int q = 0; q < kCount; ++q) load8(at8 + 8 * q * kRowThreads, v[q]);
             if (whole) {
                 unsigned listed[kCount], any = 0;
 #pragma unroll
-                for (int q = 0; q < kCount; ++q) any |= listed[q] = bytes[i + q * kSixteen];
+                for (int q = 0; q < kCount; ++q) any |= listed[q] = bytes[i + q * kRowThreads];
                 if (any) {
 #pragma unroll
                     for (int q = 0; q < kCount; ++q)
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
         const DistillRow<TL> r(p, s);
         const int b = s % kDtRows;
         TG* dz = static_cast<TG*>(p.dlogits) + r.row * p.ld;
-        for (int64_t v = (int64_t)V + tid; v < p.ld; v += kSixteen) store1(dz + v, 0.f);
+        for (int64_t v = (int64_t)V + tid; v < p.ld; v += kRowThreads) store1(dz + v, 0.f);
         mbar_wait(smem_u32(&factors_bar[b]), (uint32_t)(s / kDtRows) & 1u, abort_flag, &g_distill_status, limit_ns);
         const float mr = mr_of[b], from = -at(mr, c), factor = factor_of[b];
         const float2 from2 = make_float2(from, from), factor2 = make_float2(factor, factor);
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             constexpr int kCount = decltype(count)::value;
             float2 v[kCount][4];
 #pragma unroll
-            for (int q = 0; q < kCount; ++q) load8(at8 + 8 * q * kSixteen, v[q]);
+            for (int q = 0; q < kCount; ++q) load8(at8 + 8 * q * kRowThreads, v[q]);
             if (plain) {
 #pragma unroll
                 for (int q = 0; q < kCount; ++q)
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                                          : make_float2(0.f, 0.f);
             }
 #pragma unroll
-            for (int q = 0; q < kCount; ++q) store8(out + 8 * (i + q * kSixteen), v[q], aligned);
+            for (int q = 0; q < kCount; ++q) store8(out + 8 * (i + q * kRowThreads), v[q], aligned);
         });
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&graded_bar[b]));

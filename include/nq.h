@@ -411,7 +411,8 @@ int nq_q4_linear_fwd(const void* x, const uint32_t* Wq, const void* scales, cons
  *             elements apart (ld >= vocab: a head padded to a multiple of 128)
  *   ids     : tokens x k int32;  an id outside 0 .. vocab-1 (e.g. -1) is an absent entry, a
  *             token without entries has loss 0 and gradient 0, whatever its logits are; the
- *             masses of an id that is listed more than once add
+ *             masses of an id that is listed more than once add (a list of -inf alone, without
+ *             teacher_lse, has no softmax: NaN)
  *   teacher : tokens x k float32 (u);  teacher_lse : tokens float32 or NULL
  *   dloss   : tokens float32, the loss's weight per token (bwd)
  *   loss    : tokens float32 (written; may be NULL in bwd)
