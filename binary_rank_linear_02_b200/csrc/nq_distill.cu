@@ -207,6 +207,15 @@ struct DistillRow {
     __device__ __forceinline__ int bit(int v) const { return v - head + 8; }  // of class v: a group of 8 is a byte
 };
 
+// After a wait for a piece that was given up: the piece lands, or the fetching warp has stopped (which it
+// does when it next waits).  So a place of the ring is given back only when nothing is under way to it,
+// or nothing more will be.  (A look at the abort flag before each fetch cost 1% in place of this.)
+__device__ __noinline__ void outlast(uint32_t bar, uint32_t parity, volatile int* ended) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try(bar, parity) && !*ended && global_ns() - t0 < kWaitLimitNs) {
+    }
+}
+
 // (kTimed: a kernel of its own, since a limit that is not a constant costs the others 1%)
 template <typename TL, typename TG, bool kGrad, bool kTimed>
 __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArgs p) {
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
     __shared__ float factor_of[kDtRows], mr_of[kDtRows], scale_of[kDtRows], m_of[kDtRows], edge_z[kDtRows][16];
     __shared__ double qsum_of[kDtRows], cross_of[kDtRows], sl_of[kDtRows];
     __shared__ float ml_of[kDtRows], origin_of[kDtRows];
-    __shared__ int any_of[kDtRows], dups_of[kDtRows], abort_word;
+    __shared__ int any_of[kDtRows], dups_of[kDtRows], abort_word, stopped_word;
     volatile int* abort_flag = &abort_word;
     const int V = p.vocab, K = p.k, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float c = 1.4426950408889634f / p.temperature;
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             mbar_init(smem_u32(&factors_bar[b]), 1);
             mbar_init(smem_u32(&graded_bar[b]), kDtWarps);
         }
-        abort_word = 0;
+        abort_word = stopped_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int i = tid; i < p.rows * (int)(list_bytes / 16); i += kDtThreads)
@@ -263,8 +272,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             auto stream = [&](int i) {
                 const DistillRow<TL> r(p, i);
                 for (int first = 0; first < r.groups && ok; first += kPieceGroups) {
-                    // (a warp that gave up frees pieces without having waited for them)
-                    ok = mbar_wait(smem_u32(&empty[slot]), phase ^ 1u, abort_flag, &g_distill_status, limit_ns) && !*abort_flag;
+                    ok = mbar_wait(smem_u32(&empty[slot]), phase ^ 1u, abort_flag, &g_distill_status, limit_ns);
                     if (!ok) break;
                     const uint32_t bytes = (uint32_t)((r.groups - first < kPieceGroups ? r.groups - first : kPieceGroups) * kGroupBytes);
                     const uint32_t bar = smem_u32(&full[slot]);
@@ -281,6 +289,7 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                 if (s < n) stream(s);
                 if (kGrad && s >= p.lag) stream(s - p.lag);
             }
+            *const_cast<volatile int*>(&stopped_word) = 1;
             // whoever gave up, if any: what is in flight lands before the CTA leaves
             for (int i = issued - p.slots < 0 ? 0 : issued - p.slots; i < issued; ++i)
                 mbar_drain(smem_u32(&full[i % p.slots]), (uint32_t)(i / p.slots) & 1u);
@@ -325,21 +334,16 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
                     const int k = k0 + 32 * j;
-                    if (k - lane >= K) break;
-                    // (a class belongs to its first entry in the list, whichever lane is faster: the
-                    // order of the sum over the classes follows)
-                    const bool first = !(__match_any_sync(0xffffffffu, id[j]) & ((1u << lane) - 1u));
+                    if (k >= K) continue;
                     bool own = false;
                     if (id[j] >= 0) {
                         const int bit = r.bit(id[j]);
-                        own = first && !(atomicOr(&mask[bit >> 5], 1u << (bit & 31)) >> (bit & 31) & 1u);
+                        own = !(atomicOr(&mask[bit >> 5], 1u << (bit & 31)) >> (bit & 31) & 1u);
                         twice |= !own;
                         any = true;
                         umax = fmax(umax, (double)uk[j]);
                         zmax = fmaxf(zmax, zk[j]);
                     }
-                    __syncwarp();
-                    if (k >= K) continue;
                     sid[k] = id[j];
                     sz[k] = zk[j];
                     owner[k] = own;
@@ -349,23 +353,35 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
             any = __any_sync(0xffffffffu, any);
             twice = __any_sync(0xffffffffu, twice);
             __syncwarp();
+            // An id listed again belongs to its first entry, whichever lane was faster (the order of the
+            // sum over the classes goes by it): the entries take the bits away in turn, and put them back.
+            if (twice) {
+                for (int k = lane; k < K + lane; k += 32) {
+                    const int id = k < K ? sid[k] : -1, bit = r.bit(id);
+                    const bool first = !(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));
+                    if (id >= 0) owner[k] = first && (atomicAnd(&mask[bit >> 5], ~(1u << (bit & 31))) >> (bit & 31) & 1u);
+                    __syncwarp();
+                }
+                for (int k = lane; k < K; k += 32)
+                    if (sid[k] >= 0) atomicOr(&mask[r.bit(sid[k]) >> 5], 1u << (r.bit(sid[k]) & 31));
+                __syncwarp();
+            }
             if (lane == 0) mbar_arrive(smem_u32(&listed_bar[b]));
             double qsum = 0.0, cross = 0.0, sl = 0.0, shift = lse, esum = 0.0;  // q_k = exp(u_k / T - shift) (/ esum)
-            float ml = -INFINITY;
             if (!whole) {
                 umax = warp_max(umax);
                 shift = umax * invT;
             }
             // the logits' part of the loss is taken from the largest listed one on: where a whole row
             // is at -1e20, log p is what is left when that goes
-            zmax = (float)warp_max(zmax);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) zmax = fmaxf(zmax, __shfl_xor_sync(0xffffffffu, zmax, o));
             const float origin = fabsf(zmax) < INFINITY ? zmax : 0.f;
             for (int k = lane; k < K; k += 32) {
                 const double lq = sq[k] * invT - shift, q = sid[k] >= 0 ? exp(lq) : 0.0;
                 sq[k] = q;
                 qsum += q;
                 if (q > 0.0) cross += q * (lq - ((double)sz[k] - origin) * invT);
-                if (whole && owner[k]) ml = fmaxf(ml, sz[k]);
             }
             qsum = warp_sum(qsum);
             cross = warp_sum(cross);
@@ -375,16 +391,15 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
                 for (int k = lane; k < K; k += 32) sq[k] *= esum;
                 qsum = any ? 1.0 : 0.0;
             } else {  // the listed classes, each once
-                ml = (float)warp_max(ml);
                 for (int k = lane; k < K; k += 32)
-                    if (owner[k] && ml > -INFINITY) sl += exp(((double)sz[k] - ml) * invT);
+                    if (owner[k] && zmax > -INFINITY) sl += exp(((double)sz[k] - zmax) * invT);
                 sl = warp_sum(sl);
             }
             if (lane == 0) {
                 qsum_of[b] = qsum;
                 cross_of[b] = cross;
                 sl_of[b] = sl;
-                ml_of[b] = ml;
+                ml_of[b] = whole ? zmax : -INFINITY;  // (of the listed classes, where these are apart)
                 origin_of[b] = origin;
                 any_of[b] = any;
                 dups_of[b] = twice;
@@ -493,7 +508,8 @@ __global__ void __launch_bounds__(kDtThreads, 3) distill_kernel(const DistillArg
     // number, how many groups there are, a constant where all are).
     auto through = [&](const DistillRow<TL>& r, auto&& fn) {
         for (int first = 0; first < r.groups; first += kPieceGroups) {
-            mbar_wait(smem_u32(&full[slot]), phase, abort_flag, &g_distill_status, limit_ns);
+            if (!mbar_wait(smem_u32(&full[slot]), phase, abort_flag, &g_distill_status, limit_ns))
+                outlast(smem_u32(&full[slot]), phase, &stopped_word);
             const TL* mine = reinterpret_cast<const TL*>(smem + slot * kDtPiece) + 8 * tid;
             const int left = r.groups - first - tid;
             if (r.groups - first >= kPieceGroups) {
