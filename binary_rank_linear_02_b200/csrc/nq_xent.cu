@@ -9,9 +9,13 @@
 // a piece's z is computed again, its epilogue writes dz as bfloat16 into a scratch of bounded
 // size, and two products read it: the piece's rows of dW (complete, since they sum over the
 // tokens) and its share of dh (summed over the pieces in fp32, in order).  dz in bfloat16 is
-// what lets both products run on the bf16 tensor cores (an operand pair has one type): its
-// rounding is at most 2^-8 of each term, of the same size as the rounding of the bfloat16 results.
-// With few tokens, where these roundings do not average out, dz is two bfloat16 parts.
+// what lets both products run on the bf16 tensor cores (an operand pair has one type).  Its rounding,
+// at most 2^-8 of each term, would be as large as that of the bfloat16 results, and nearly all of it
+// at the labels, whose terms are the large ones: what bfloat16 leaves there is kept in fp32, a number
+// a token, and added to dh and dW in the products' epilogues (their error in the norm is then the
+// results' own rounding, 1.66e-3, where it was 2.4e-3; 1000 tokens x 50257 x 2048 backward: 524 to 544 us,
+// 4096 x 32000 x 4096: 2% more).  With few tokens, where the others' roundings do not average out, dz is
+// two bfloat16 parts; for dW also with many tokens per class, see many_per_class().
 //
 // All four products are the same tcgen05 kernel (kind::f16, bf16 operands, fp32 accumulators)
 // with other operand orders and epilogues: dW reads dz and h token-major (MN-major tiles), dh
@@ -19,13 +23,13 @@
 // multiples of the tile: TMA fills with zeros outside, epilogues mask.
 //
 // What bounds it: the tensor cores, from some 256 tokens on.  4096 tokens x 32000 classes x 4096:
-// forward 757 us (1419 TFLOP/s; cuBLAS, kept busy for seconds, reaches 1407 under the power cap),
-// backward, with z computed again, 2365 us (1362).  Hence pairs of CTAs (half of B's traffic in
+// forward 780 to 811 us (1376 to 1324 TFLOP/s; cuBLAS, kept busy for seconds, reaches 1407 under the power
+// cap), backward, with z computed again, 2430 to 2550 us (1325 to 1263).  Hence pairs of CTAs (half of B's traffic in
 // shared memory) and two accumulators (one CTA with a 128 x 256 tile took 1029 and 3756 us).  The
 // epilogue has to be done within a tile's MMAs, some 13 us at d = 4096: eight warps a CTA, label
 // and ignored tokens outside the loop over the columns, results written by way of shared memory
 // as rows of 128 bytes (from the lanes, each its own row, they came in pieces of 16 bytes: four
-// such warps took 556 us where these take 521, 1000 tokens x 50257 x 2048 backward).
+// such warps took 556 us where these took 525, 1000 tokens x 50257 x 2048 backward).
 // With few tokens HBM bounds it, W's bytes: see kXFewTokens.
 //
 // The tensor cores round an accumulator toward zero at each step of 16 products, so a sum of
@@ -139,16 +143,32 @@ enum { kStats = 0, kDz = 1, kToBf16 = 2, kPartial = 3 };
 // elements of d), columns are tokens.
 struct XentEpilogue {
     int64_t rows, cols;     // of the product (unpadded)
-    const int32_t* labels;  // kStats, kDz: per token
-    int64_t label0, vocab;  // first class of the product; all classes
-    float2* stats;          // kStats: [token][slot]: maximum, sum of exp(z - maximum)
-    int slots;
-    float* picked;          // kStats: z of the label, per token
+    const int32_t* labels;  // per token
+    int64_t label0;         // first class of the product
+    union {
+        int64_t vocab;      // all classes (kPartial: those up to the product's end)
+        int64_t tokens;     // kToBf16: how many labels there are
+    };
+    // rest, not kStats: what bf16 leaves of dz at each token's label, fp32 (null: it is not kept apart).
+    // kDz writes it; kPartial (dh) adds it times the label's row of W, kToBf16 (dW) times the token's row
+    // of h, to the class's row.
+    union {
+        float2* stats;      // kStats: [token][slot]: maximum, sum of exp(z - maximum)
+        float* rest;
+    };
+    union {
+        int slots;
+        int rest_pitch;     // floats from one token's rest to the next
+    };
+    union {
+        float* picked;      // kStats: z of the label, per token
+        const uint16_t* other;  // the rows that rest is multiplied by, as long as the product's
+    };
     const float* lse;       // kDz, per token
     const float* dloss;     // kDz, per token
     uint16_t* out;          // kDz, kToBf16: bf16, [row][column] with pitch ldo (kT: [column][row])
     int64_t ldo;
-    int low;                // kDz, kT: what bf16 leaves of dz goes this many columns on (0: nowhere)
+    int low;                // kDz: what bf16 leaves of dz goes this many rows (kT: columns) on (0: nowhere)
     float* part;            // kPartial: [split][row][column] fp32 (kT: [split][column][row]), added to unless first
     int first;
 };
@@ -179,6 +199,15 @@ __device__ __forceinline__ XentToken xent_token(const XentEpilogue& e, int64_t t
             }
         }
     }
+    if constexpr (kEpi == kPartial) {  // the label's row in `other` and what its dz is to be made up by
+        if (there && e.rest) {
+            const int64_t label = e.labels[token];
+            if (label >= e.label0 && label < e.vocab) {
+                t.label = (int)(label - e.label0);
+                t.dl = e.rest[token * e.rest_pitch];
+            }
+        }
+    }
     return t;
 }
 
@@ -200,13 +229,13 @@ __device__ __forceinline__ void staging_put(uint32_t buffer, int lane, int piece
                  ::"r"(buffer + (uint32_t)(lane * 128 + ((piece ^ (lane & 7)) << 4))), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
-template <typename Fn>
+template <int kPieces = 8, typename Fn>
 __device__ __forceinline__ void staging_write(uint32_t buffer, int lane, Fn&& fn) {
     __syncwarp();
-    const int piece = lane & 7;
+    const int piece = lane % kPieces;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
+    for (int i = 0; i < kPieces; ++i) {
+        const int r = 32 / kPieces * i + lane / kPieces;
         uint4 v;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -293,6 +322,158 @@ __device__ __forceinline__ void xent_dz32(float (&v)[32], int at, const XentToke
     for (int j = 0; j < 32; ++j) v[j] *= tok.dl;
 }
 
+// What bf16 leaves of a number.
+__device__ __forceinline__ float xent_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float xent_float(uint16_t bits) { return __uint_as_float((uint32_t)bits << 16); }
+
+// What a warp needs to find the tokens whose labels are among its 32 classes (lane = class).
+struct XentLabels {
+    const int32_t* labels;
+    const float* rest;
+    const uint16_t* h;  // tokens' rows
+    int64_t cols;
+    int tokens, rest_pitch, first, limit;  // limit: how many of the 32 there are
+};
+__device__ __forceinline__ XentLabels xent_labels(const XentEpilogue& e, int64_t row0) {
+    const int64_t rows = e.rows - row0;
+    return XentLabels{e.labels, e.rest, e.other, e.cols, (int)e.tokens, e.rest_pitch, (int)(e.label0 + row0),
+                      rows < 32 ? (int)(rows > 0 ? rows : 0) : 32};
+}
+// Goes through the labels from token `from` on, in order: fn(token, class), the same in all lanes, for those
+// found; before a group of 32 tokens in which `room` has none left it stops, and returns where.
+// `label` holds those of the 256 tokens from `from` on.
+__device__ __forceinline__ void xent_load_labels(const int32_t* labels, int tokens, int from, int lane, int (&label)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int i = from + 32 * u + lane;
+        label[u] = i < tokens ? labels[i] : -1;
+    }
+}
+template <typename Room, typename Fn>
+__device__ __forceinline__ int xent_search(const XentLabels& e, int (&label)[8], int from, int lane, Room&& room, Fn&& fn) {
+    while (from < e.tokens) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int at = label[u] - e.first;
+            unsigned hits = __ballot_sync(0xffffffffu, label[u] >= 0 && at >= 0 && at < e.limit);
+            if (hits) {
+                if (!room(__popc(hits))) return from + 32 * u;
+                for (; hits; hits &= hits - 1) {
+                    const int l = __ffs(hits) - 1;
+                    fn(from + 32 * u + l, __shfl_sync(0xffffffffu, at, l));
+                }
+            }
+        }
+        from += 256;
+        if (from < e.tokens) xent_load_labels(e.labels, e.tokens, from, lane, label);
+    }
+    return e.tokens;
+}
+// The tokens of a lane's class, if no class of the warp has more than kXOwn.
+constexpr int kXOwn = 4;
+struct XentMatches {
+    int most;          // that a class has
+    int token[kXOwn];  // of this lane's (-1: none)
+    float rest[kXOwn];
+};
+__device__ __forceinline__ XentMatches xent_matches(const XentLabels& e, const int (&first)[8], int64_t col0, int lane) {
+    XentMatches m;
+#pragma unroll
+    for (int k = 0; k < kXOwn; ++k) {
+        m.token[k] = -1;
+        m.rest[k] = 0.f;
+    }
+    int mine = 0, label[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) label[u] = first[u];
+    xent_search(e, label, 0, lane, [](int) { return true; }, [&](int token, int row) {
+        if (lane == row) {
+#pragma unroll
+            for (int k = 0; k < kXOwn; ++k)
+                if (mine == k) m.token[k] = token;
+            ++mine;
+        }
+    });
+    m.most = __reduce_max_sync(0xffffffffu, mine);
+#pragma unroll
+    for (int k = 0; k < kXOwn; ++k) {
+        if (m.token[k] < 0) break;
+        m.rest[k] = e.rest[(int64_t)m.token[k] * e.rest_pitch];
+        // the lines of h that the epilogue is to read, on their way while the sums are
+        const uint16_t* h = e.h + (int64_t)m.token[k] * e.cols;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int64_t at = col0 + (i < 2 ? 64 * i : 127);
+            asm volatile("{\n.reg .b16 t;\nld.global.ca.b16 t, [%0];\n}" ::"l"(h + (at < e.cols ? at : e.cols - 1)) : "memory");
+        }
+    }
+    return m;
+}
+
+// Adds up, for a warp's 32 x 32 part of dW, what its classes' tokens are to be made up by, in the order of the
+// tokens: in shared memory, a column to a lane (element (r, c) in place c ^ r of row r).  For classes that
+// are many tokens' labels; 32 tokens at a time.
+__device__ __noinline__ void xent_make_up(const XentLabels& e, int64_t col, uint32_t buffer, int lane) {
+    for (int r = 0; r < 32; ++r) asm volatile("st.shared.f32 [%0], %1;" ::"r"(buffer + (uint32_t)(128 * r + 4 * lane)), "f"(0.f) : "memory");
+    const bool there = col + lane < e.cols;
+    const uint16_t* h = e.h + col + lane;
+    for (int from = 0; from < e.tokens;) {
+        int count = 0, token = 0, row = 0;  // (one to a lane)
+        int label[8];
+        xent_load_labels(e.labels, e.tokens, from, lane, label);
+        from = xent_search(e, label, from, lane, [&](int more) { return count + more <= 32; }, [&](int t, int r) {
+            if (lane == count) {
+                token = t;
+                row = r;
+            }
+            ++count;
+        });
+        const float rest = lane < count ? e.rest[(int64_t)token * e.rest_pitch] : 0.f;
+        float x[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+            const int t = __shfl_sync(0xffffffffu, token, u);
+            x[u] = there && u < count ? xent_float(h[(int64_t)t * e.cols]) : 0.f;
+        }
+        // (a class that comes again at once is added up in a register: one that most tokens have costs their loads)
+        int at_row = -1;
+        uint32_t at = 0;
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+            const int r = __shfl_sync(0xffffffffu, row, u);
+            const float part = __shfl_sync(0xffffffffu, rest, u);
+            if (u >= count) break;
+            if (r != at_row) {
+                if (at_row >= 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(sum) : "memory");
+                at_row = r;
+                at = buffer + (uint32_t)(128 * r + 4 * (lane ^ r));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sum) : "r"(at) : "memory");
+            }
+            sum = fmaf(part, x[u], sum);
+        }
+        if (at_row >= 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(sum) : "memory");
+    }
+    __syncwarp();
+}
+
+// v += a times 32 bf16 numbers (left of them; a multiple of 8).
+__device__ __forceinline__ void xent_add32(float (&v)[32], float a, const uint16_t* row, int left) {
+    uint4 x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        x[q] = 8 * q < left ? *reinterpret_cast<const uint4*>(row + 8 * q) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t two[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[8 * q + 2 * i] = fmaf(a, __uint_as_float(two[i] << 16), v[8 * q + 2 * i]);
+            v[8 * q + 2 * i + 1] = fmaf(a, __uint_as_float(two[i] & 0xFFFF0000u), v[8 * q + 2 * i + 1]);
+        }
+    }
+}
+
 // The transposed product's 32 columns (tokens, from `col` on, n of them) of the warp's 32 rows
 // (classes, or elements of d; lane = row); tok: of token col + lane.
 template <int kEpi>
@@ -315,14 +496,25 @@ __device__ __forceinline__ void xent_columns_t(const XentEpilogue& e, float (&v)
         const float sum = across_lanes(v, lane, [](float a, float b) { return a + b; });
         if (lane < n) e.stats[(col + lane) * e.slots + slot] = make_float2(top, sum);
     } else {
+        [[maybe_unused]] uint16_t w[32];  // (what bf16 left of dz at the tokens' labels is to be multiplied by)
+        if constexpr (kEpi == kPartial) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int label = __shfl_sync(0xffffffffu, tok.label, j);
+                w[j] = label >= 0 && there ? e.other[(int64_t)label * e.rows + row] : 0;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             float x = v[j];
+            if constexpr (kEpi == kPartial) x = fmaf(__shfl_sync(0xffffffffu, tok.dl, j), xent_float(w[j]), x);
             if constexpr (kEpi == kDz) {
                 const float p = xent_ex2(fmaf(x, kLog2e, -__shfl_sync(0xffffffffu, tok.lse2, j)));
                 const float dl = __shfl_sync(0xffffffffu, tok.dl, j);
-                x = (p - (__shfl_sync(0xffffffffu, tok.label, j) == cls ? 1.f : 0.f)) * dl;
+                const bool labelled = __shfl_sync(0xffffffffu, tok.label, j) == cls;
+                x = (p - (labelled ? 1.f : 0.f)) * dl;
                 x = dl == 0.f || j >= n ? 0.f : x;
+                if (e.rest && labelled && there && j < n) e.rest[(col + j) * (int64_t)e.rest_pitch] = xent_rest(x);
                 if (e.low && there && col + j < e.low) {  // (columns after the last: zeros)
                     const __nv_bfloat16 high = __float2bfloat16_rn(x);
                     e.out[(col + j) * e.ldo + row] = __bfloat16_as_ushort(high);
@@ -344,8 +536,8 @@ __device__ __forceinline__ void xent_columns_t(const XentEpilogue& e, float (&v)
 
 // An epilogue warp's share of a tile: its 32 rows (from row0 on), 128 columns from col0 on.
 template <int kEpi>
-__device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr, int64_t row0, int64_t col0, int64_t split,
-                                          const XentToken& tok, uint32_t buffer, int lane) {
+__device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr, int64_t row0, int64_t col0, int split, int splits,
+                                          const XentToken& tok, const XentMatches& matches, uint32_t buffer, int lane) {
     const int left = (int)(e.cols - col0 < 128 ? e.cols - col0 : 128);
     int at = -1 << 20;  // the label's column from col0 on
     if constexpr (kEpi == kDz) {
@@ -357,13 +549,15 @@ __device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr,
         for (int c0 = 0; c0 < left; c0 += 32) {
             float v[32];
             xent_load32(taddr + (uint32_t)c0, v);
+            if (tok.label >= 0 && ((col0 + c0) >> 5) % splits == split)  // (what bf16 left of dz there: by one share of the sum)
+                xent_add32(v, tok.dl, e.other + (int64_t)tok.label * e.cols + col0 + c0, left - c0);
 #pragma unroll
             for (int p = 0; p < 8; ++p)
                 staging_put(buffer, lane, p, make_uint4(__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]),
                                                         __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3])));
             staging_write(buffer, lane, [&](int r, int p, uint4 w) {
                 if (row0 + r >= e.rows || c0 + 4 * p >= left) return;  // (cols is a multiple of 8)
-                float4* a = reinterpret_cast<float4*>(e.part + (split * e.rows + row0 + r) * e.cols + col0 + c0 + 4 * p);
+                float4* a = reinterpret_cast<float4*>(e.part + ((int64_t)split * e.rows + row0 + r) * e.cols + col0 + c0 + 4 * p);
                 float4 x = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
                 if (!e.first) {
                     const float4 o = *a;
@@ -376,13 +570,66 @@ __device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr,
             });
         }
     } else {
+        if constexpr (kEpi == kToBf16) {
+            if (matches.most > kXOwn) {  // (the staging serves the sums first, then half as wide rows of results)
 #pragma unroll 1
-        for (int c0 = 0; c0 < left; c0 += 64) {
+                for (int c0 = 0; c0 < left; c0 += 32) {
+                    xent_make_up(xent_labels(e, row0), col0 + c0, buffer, lane);
+                    float v[32];
+                    xent_load32(taddr + (uint32_t)c0, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float x;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(buffer + (uint32_t)(128 * lane + 4 * (j ^ lane))) : "memory");
+                        v[j] += x;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        staging_put(buffer, lane, p,
+                                    make_uint4(xent_pack(v[8 * p], v[8 * p + 1]), xent_pack(v[8 * p + 2], v[8 * p + 3]),
+                                               xent_pack(v[8 * p + 4], v[8 * p + 5]), xent_pack(v[8 * p + 6], v[8 * p + 7])));
+                    staging_write<4>(buffer, lane, [&](int r, int p, uint4 w) {
+                        if (row0 + r < e.rows && c0 + 8 * p < left)
+                            *reinterpret_cast<uint4*>(e.out + (row0 + r) * e.ldo + col0 + c0 + 8 * p) = w;
+                    });
+                }
+                return;
+            }
+        }
+        // (dz in two parts: its second one by going through the tile again)
+        const bool two = kEpi == kDz && e.low != 0;
+#pragma unroll 1
+        for (int c = 0; c < (two ? 256 : 128); c += 64) {
+            const int c0 = c & 127;
+            if (c0 >= left) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 float v[32];
                 xent_load32(taddr + (uint32_t)(c0 + 32 * half), v);
-                if constexpr (kEpi == kDz) xent_dz32(v, at - c0 - 32 * half, tok);
+                if constexpr (kEpi == kDz) {
+                    const int a = at - c0 - 32 * half;
+                    xent_dz32(v, a, tok);
+                    if (e.rest && (unsigned)a < 32u) {
+                        float x = v[0];
+#pragma unroll
+                        for (int j = 1; j < 32; ++j) x = j == a ? v[j] : x;
+                        e.rest[(row0 + lane) * e.rest_pitch] = xent_rest(x);
+                    }
+                    if (c >= 128) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = xent_rest(v[j]);
+                    }
+                }
+                if constexpr (kEpi == kToBf16) {
+#pragma unroll
+                    for (int k = 0; k < kXOwn; ++k) {
+                        if (k >= matches.most) break;
+                        if (matches.token[k] >= 0)
+                            xent_add32(v, matches.rest[k], e.other + (int64_t)matches.token[k] * e.cols + col0 + c0 + 32 * half,
+                                       left - c0 - 32 * half);
+                    }
+                }
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
                     staging_put(buffer, lane, 4 * half + p,
@@ -392,7 +639,7 @@ __device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr,
             staging_write(buffer, lane, [&](int r, int p, uint4 w) {
                 // (dz: whole tiles, its rows are as long; dW, dh: cols is a multiple of 8)
                 if (row0 + r >= e.rows || (kEpi == kToBf16 && c0 + 8 * p >= left)) return;
-                *reinterpret_cast<uint4*>(e.out + (row0 + r) * e.ldo + col0 + c0 + 8 * p) = w;
+                *reinterpret_cast<uint4*>(e.out + (row0 + r + (c >= 128 ? e.low : 0)) * e.ldo + col0 + c0 + 8 * p) = w;
             });
         }
     }
@@ -588,12 +835,21 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
         const uint32_t buffer = base + (uint32_t)(kXSpace - kXStaging + (warp - 4) * kXStagingBytes);
         int n = 0;
         bool ok = true;
+        [[maybe_unused]] int first_labels[8];  // (looked through for every tile)
+        if constexpr (kEpi == kToBf16 && !kT) {
+            if (e.rest) xent_load_labels(e.labels, (int)e.tokens, 0, lane, first_labels);
+        }
         for (int item = pair; item < items && ok; item += pairs) {
             int tm, tn, kb0, kb1;
             const int split = tile_of(item, tm, tn, kb0, kb1);
             const int64_t row0 = (int64_t)tm * kXTile + (int)rank * kXHalfTile + quad * 32;
             const int64_t col0 = (int64_t)tn * kXTile + 128 * half;  // (not transposed)
             XentToken tok = xent_token<kEpi>(e, row0 + lane, !kT && row0 + lane < e.rows);
+            XentMatches matches;
+            matches.most = 0;
+            if constexpr (kEpi == kToBf16 && !kT) {  // (while the sums are under way)
+                if (e.rest) matches = xent_matches(xent_labels(e, row0), first_labels, col0, lane);
+            }
             [[maybe_unused]] float z[128];  // (the sum of a tile's parts, where it may have several)
             if constexpr (kKeeps) {
 #pragma unroll
@@ -615,7 +871,8 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                         const int64_t col = (int64_t)tn * columns + c0, left = e.cols - col;
                         const int room = columns - c0 < 32 ? columns - c0 : 32, here = left < room ? (int)left : room;
                         if (here <= 0) break;
-                        tok = xent_token<kEpi>(e, col + lane, lane < here);
+                        // (dh: what bf16 left of dz is added by one of the sum's shares, of 32 columns at a time)
+                        tok = xent_token<kEpi>(e, col + lane, lane < here && (kEpi != kPartial || (c0 >> 5) % plan.splits == split));
                         float v[32];
                         xent_load32(taddr + (uint32_t)c0, v);
                         for (int i = 1; i < accs; ++i) {
@@ -642,7 +899,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                         for (int j = 0; j < 32; ++j) z[c0 + j] += v[j];
                     }
                 } else {
-                    xent_rows<kEpi>(e, taddr + (uint32_t)(128 * half), row0, col0, split, tok, buffer, lane);
+                    xent_rows<kEpi>(e, taddr + (uint32_t)(128 * half), row0, col0, split, plan.splits, tok, matches, buffer, lane);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -791,7 +1048,7 @@ int xent_launch(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, 
 
 // Up to this many tokens the products with W are transposed: W's rows (or columns) are the
 // tile's 256 rows, and all tokens fit its columns, of which only as many as needed are summed.
-// (8 tokens x 32000 x 4096: 53 us, W at 5.0 TB/s, where tiles of 256 tokens took 73.)  Where the
+// (8 tokens x 32000 x 4096: 53 us, W at 4.9 TB/s, where tiles of 256 tokens took 73.)  Where the
 // columns leave room, a tile has two or four accumulators: the tensor cores round a sum down
 // after each step, and shorter sums lose less (a few 1e-7 of a loss in place of 1e-6).
 constexpr int64_t kXFewTokens = 256;
@@ -802,11 +1059,26 @@ int few_columns(int64_t tokens) { return (int)round_up(tokens, 16); }
 // per tile of W, dW twice the K blocks.
 constexpr int64_t kXTwoParts = 128;
 int low_rows(int64_t tokens) { return tokens <= kXTwoParts ? few_columns(tokens) : 0; }
-int64_t dz_rows(int64_t tokens) { return tokens <= kXTwoParts ? 2 * few_columns(tokens) : tokens; }
+// Above, dW's epilogue looks for the tokens of its classes, to add what bfloat16 left of dz there.  With more
+// tokens than half the classes it would find too many (4096 tokens x 500 x 4096: 456 us, 4096 x 2000 x 2048:
+// 243, where the calls take 68 and 90 with nothing added): there dz is two parts for dW too, whose K blocks
+// double (122 and 134 us); with fewer, hardly a warp has a class of more than the four that it keeps in
+// registers.  Two parts of 256 classes have to fit dz's scratch; with more tokens than that dW is without.
+constexpr int64_t kXTwoPartsMost = kXPieceBytes / (2 * 2 * kXTile);
+bool many_per_class(int64_t tokens, int64_t vocab) { return tokens > kXTwoParts && 2 * tokens > vocab; }
+// Rows (of tokens) after which dz's second part begins (0: it has none).
+int dz_low(int64_t tokens, int64_t vocab) {
+    if (!many_per_class(tokens, vocab)) return low_rows(tokens);
+    return tokens > kXTwoPartsMost ? 0 : tokens <= kXFewTokens ? few_columns(tokens) : (int)tokens;
+}
+int64_t dz_rows(int64_t tokens, int64_t vocab) {
+    const int low = dz_low(tokens, vocab);
+    return low ? 2 * low : tokens;
+}
 
 // Classes per piece of the backward: as many whole column tiles as dz's scratch holds.
 int64_t piece_classes(int64_t tokens, int64_t vocab) {
-    const int64_t fit = kXPieceBytes / (2 * dz_rows(tokens)) / kXTile * kXTile;
+    const int64_t fit = kXPieceBytes / (2 * dz_rows(tokens, vocab)) / kXTile * kXTile;
     const int64_t all = round_up(vocab, kXTile);
     return fit < kXTile ? kXTile : fit < all ? fit : all;
 }
@@ -842,7 +1114,7 @@ BackwardPlan plan_backward(int64_t tokens, int64_t vocab, int64_t d) {
     BackwardPlan p;
     p.piece = piece_classes(tokens, vocab);
     p.splits = dh_splits(tokens, p.piece < vocab ? p.piece : vocab, d);
-    p.direct = p.piece >= vocab && p.splits == 1;
+    p.direct = p.piece >= vocab && p.splits == 1 && tokens <= kXTwoParts;  // (else made up: see rest)
     return p;
 }
 
@@ -860,7 +1132,7 @@ int64_t xent_fwd_scratch_bytes(int64_t tokens, int64_t vocab) {
 
 int64_t xent_bwd_scratch_bytes(int64_t tokens, int64_t vocab, int64_t d) {
     const BackwardPlan p = plan_backward(tokens, vocab, d);
-    return round_up(2 * dz_rows(tokens) * p.piece, 256) + (p.direct ? 0 : round_up(4 * p.splits * tokens * d, 256));
+    return round_up(2 * dz_rows(tokens, vocab) * p.piece, 256) + (p.direct ? 0 : round_up(4 * p.splits * tokens * d, 256));
 }
 
 // z of tokens and classes (nv rows of W), its epilogue kEpi: stats or dz.
@@ -888,9 +1160,12 @@ static int xent_dh(const uint16_t* dz, int64_t piece, const uint16_t* W, int64_t
         return xent_launch<kEpi, true, false, true>(W, d, dz, piece, d, low ? 2 * low : tokens, nv,
                                                     low ? 2 * low : few_columns(tokens), splits, false, e, stream, low);
     }
-    e.rows = tokens;
-    e.cols = d;
-    return xent_launch<kEpi, false, true, false>(dz, piece, W, d, tokens, d, nv, kXTile, splits, false, e, stream);
+    if constexpr (kEpi == kPartial) {
+        e.rows = tokens;
+        e.cols = d;
+        return xent_launch<kEpi, false, true, false>(dz, piece, W, d, tokens, d, nv, kXTile, splits, false, e, stream);
+    }
+    return NQ_ERR_SHAPE;  // (as bf16 at once: few tokens alone)
 }
 
 int xent_forward(const uint16_t* h, const uint16_t* W, const int32_t* labels, int64_t tokens, int64_t vocab, int64_t d,
@@ -916,7 +1191,7 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
     const BackwardPlan plan = plan_backward(tokens, vocab, d);
     const int64_t piece = plan.piece;
     uint16_t* dz = static_cast<uint16_t*>(scratch);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(2 * dz_rows(tokens) * piece, 256));
+    float* part = reinterpret_cast<float*>(static_cast<char*>(scratch) + round_up(2 * dz_rows(tokens, vocab) * piece, 256));
     for (int64_t v0 = 0; v0 < vocab; v0 += piece) {
         const int64_t nv = vocab - v0 < piece ? vocab - v0 : piece;
         XentEpilogue e = {};
@@ -927,7 +1202,13 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
         e.dloss = dloss;
         e.out = dz;
         e.ldo = piece;
-        e.low = low_rows(tokens);
+        e.low = dz_low(tokens, vocab);
+        // above kXTwoParts tokens what bf16 leaves of dz at the labels: in dh's rows, which are written last,
+        // or, with dW alone, where dh's sums would be
+        if (tokens > kXTwoParts) {
+            e.rest = dh ? reinterpret_cast<float*>(dh) : part;
+            e.rest_pitch = dh ? (int)(d / 2) : 1;
+        }
         int rc = xent_logits<kDz>(h, W + v0 * d, tokens, nv, d, e, stream);
         if (rc != NQ_OK) return rc;
         if (dW) {
@@ -936,7 +1217,15 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
             g.cols = d;
             g.out = dW + v0 * d;
             g.ldo = d;
-            rc = xent_launch<kToBf16, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream, low_rows(tokens));
+            if (!many_per_class(tokens, vocab)) {
+                g.labels = labels;
+                g.label0 = v0;
+                g.rest = e.rest;
+                g.rest_pitch = e.rest_pitch;
+                g.other = h;
+                g.tokens = tokens;
+            }
+            rc = xent_launch<kToBf16, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream, e.low);
             if (rc != NQ_OK) return rc;
         }
         if (dh) {
@@ -949,6 +1238,12 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
                 // the last piece may have fewer K blocks than shares: then it adds to the first ones
                 g.part = part;
                 g.first = v0 == 0;
+                g.labels = labels;
+                g.label0 = v0;
+                g.vocab = v0 + nv;
+                g.rest = e.rest;
+                g.rest_pitch = e.rest_pitch;
+                g.other = W + v0 * d;
                 const int64_t nkb = cut(nv, kXK), per = cut(nkb, plan.splits);
                 rc = xent_dh<kPartial>(dz, piece, W + v0 * d, tokens, nv, d, (int)cut(nkb, per), g, stream);
             }

@@ -452,8 +452,9 @@ int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const i
  * lse by the largest ez of its row and (vocab/32 + 64 + |lse|) 2^-23, loss by twice that and its label's
  * part of it.  Backward: z is computed again, p = exp(z - lse) in fp32 from the lse that is given; dz passes
  * through bfloat16 (the operand type of the tensor cores beside h and W), up to 128 tokens as two
- * bfloat16 parts; sums over classes and tokens are fp32; results are rounded once to bfloat16.  With
- * r = 2^-8, or 2^-16 up to 128 tokens,
+ * bfloat16 parts; what it leaves at the labels, which are nearly all of dz in the norm, is added in fp32;
+ * sums over classes and tokens are fp32; results are rounded once to bfloat16.  With r = 2^-8 (2^-16 up
+ * to 128 tokens; 2^-16 at v = labels[i], but for dW of more than 2^18 tokens and more than vocab / 2),
  *     |error of dz_iv| <= r |dz_iv| + |dloss_i| (p_iv (2 ez + 2^-18) + 2^-23) =: edz,
  *     |error of dh_ij| <= sum_v edz_iv |W_vj| + (vocab/8 + 32) 2^-23 sum_v |dz_iv W_vj| + 2^-8 |dh_ij|,
  * the last two up to a factor of 1 + 2^-6, likewise dW with sums over the tokens.  (The 2^-23 counts

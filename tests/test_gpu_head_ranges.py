@@ -144,3 +144,100 @@ def test_cross_entropy_tokens_past_four_gigabytes(nq):
         ref = dz @ Wd
         bound = edz @ Wd.abs() + (vocab / 8 + 32) * U * (dz.abs() @ Wd.abs()) + BF * ref.abs()
         assert torch.all((dh[rows].double() - ref).abs() <= bound * (1 + 2.0 ** -6) + 1e-38)
+
+
+@pytest.mark.parametrize("tokens,vocab,d,kind", [
+    (129, 1, 8, "even"), (129, 700, 72, "even"), (200, 5, 264, "even"), (256, 32, 1000, "one"), (257, 1000, 64, "even"),
+    (300, 40, 136, "even"), (600, 40, 520, "even"), (600, 5000, 200, "some"), (1000, 3001, 256, "some"), (2050, 700, 136, "even"),
+    (1100, 300, 264, "one"), (4100, 40000, 64, "some"), (3000, 257, 1032, "few")])
+def test_cross_entropy_labels_are_kept_apart(nq, tokens, vocab, d, kind):
+    """Above 128 tokens dz is bfloat16 but at the labels, whose rest is added in fp32 (off by 2^-24 of the
+    entry beside the logits' error): to dh each token's own, to dW those of a class's tokens, none, a few,
+    or more than are kept in registers (4) and than are looked for at a time (32)."""
+    g = torch.Generator(device="cuda").manual_seed(41)
+    h = torch.randn(tokens, d, device="cuda", generator=g).bfloat16()
+    W = (torch.randn(vocab, d, device="cuda", generator=g) * (1.6 / d ** 0.5)).bfloat16()
+    labels = torch.randint(0, vocab, (tokens,), device="cuda", generator=g, dtype=torch.int32)
+    if kind == "some":  # classes of one, two, ... tokens beside each other
+        labels[: tokens // 4] = labels[: tokens // 4] % 20
+    if kind == "few":  # three classes far apart
+        labels = torch.tensor([0, vocab // 2, vocab - 1], device="cuda", dtype=torch.int32)[labels % 3]
+    if kind == "one":
+        labels[:] = vocab - 1
+    labels[3::11] = -100
+    labels[5::13] = vocab  # do not count either
+    dloss = torch.rand(tokens, device="cuda", generator=g) + 0.1
+    loss, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    dh, dW = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    counted = (labels >= 0) & (labels < vocab)
+    hd, Wd = h.double(), W.double()
+    dl = torch.where(counted, dloss, 0.0).double()[:, None]
+    z = hd @ Wd.T
+    ez = (d / 16 + 16) * U * (hd.abs() @ Wd.abs().T)
+    p = torch.exp(z - lse.double()[:, None])
+    dz = p * dl
+    rows = torch.arange(tokens, device="cuda")[counted]
+    at = labels[counted].long()
+    dz[rows, at] -= dl[counted, 0]
+    stored = 2.0 ** -8 * dz.abs()
+    stored[rows, at] = 2.0 ** -23 * dz[rows, at].abs()
+    edz = stored + dl * (p * (2 * ez + 2.0 ** -18) + 2.0 ** -23)
+    for got, e, x, b, terms in ((dh, edz, dz, Wd, vocab), (dW, edz.T, dz.T, hd, tokens)):
+        ref = x @ b
+        bound = e @ b.abs() + (terms / 8 + 32) * U * (x.abs() @ b.abs()) + BF * ref.abs()
+        assert torch.all((got.double() - ref).abs() <= bound * (1 + 2.0 ** -6) + 1e-38)
+    alone, none = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss, need_dW=False)
+    assert torch.equal(alone, dh)
+    none, alone = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss, need_dh=False)
+    assert torch.equal(alone, dW)
+
+
+@pytest.mark.parametrize("tokens,vocab,d", [(129, 2000, 512), (300, 5003, 520), (1000, 3001, 1024), (2050, 700, 136)])
+def test_cross_entropy_gradients_lose_little_beside_their_rounding(nq, tokens, vocab, d):
+    """dh's and dW's relative error in the norm: that of rounding them to bfloat16 (below 2^-9, about 0.29 of a
+    step of 2^-7, as errors spread evenly) and little more, since what bfloat16 dz adds is its classes'
+    beside the labels': below 2^-8 sqrt(sum p^2) of the norm, with sum p^2 of these logits below 0.05."""
+    g = torch.Generator(device="cuda").manual_seed(42)
+    h = torch.randn(tokens, d, device="cuda", generator=g).bfloat16()
+    W = (torch.randn(vocab, d, device="cuda", generator=g) * (1.6 / d ** 0.5)).bfloat16()
+    labels = torch.randint(0, vocab, (tokens,), device="cuda", generator=g, dtype=torch.int32)
+    dloss = torch.rand(tokens, device="cuda", generator=g) + 0.5
+    _, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    got = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    p = torch.softmax(h.double() @ W.double().T, 1)
+    assert float((p * p).sum(1).mean()) < 0.05
+    dz = p * dloss.double()[:, None]
+    dz[torch.arange(tokens, device="cuda"), labels.long()] -= dloss.double()
+    for x, ref in zip(got, (dz @ W.double(), dz.T @ h.double())):
+        rounded = (ref.bfloat16().double() - ref).norm()
+        assert float((x.double() - ref).norm()) <= float(1.1 * rounded + 2.0 ** -8 * 0.05 ** 0.5 * 0.5 * ref.norm())
+
+
+@pytest.mark.parametrize("tokens,kept", [(262144, True), (262400, False)])
+def test_cross_entropy_many_tokens_of_few_classes(nq, tokens, kept):
+    """dW of so many tokens per class: up to 2^18 of them dz is two parts (off by 2^-16), beyond it is one."""
+    vocab, d = 100, 16
+    g = torch.Generator(device="cuda").manual_seed(43)
+    h = torch.randn(tokens, d, device="cuda", generator=g).bfloat16()
+    W = torch.randn(vocab, d, device="cuda", generator=g).bfloat16()
+    labels = torch.randint(-1, vocab, (tokens,), device="cuda", generator=g, dtype=torch.int32)
+    dloss = torch.rand(tokens, device="cuda", generator=g) + 0.1
+    _, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    dh, dW = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    hd, Wd = h.double(), W.double()
+    dl = torch.where(labels >= 0, dloss, 0.0).double()[:, None]
+    z = hd @ Wd.T
+    ez = (d / 16 + 16) * U * (hd.abs() @ Wd.abs().T)
+    p = torch.exp(z - lse.double()[:, None])
+    dz = p * dl
+    rows = torch.arange(tokens, device="cuda")[labels >= 0]
+    at = labels[rows].long()
+    dz[rows, at] -= dl[rows, 0]
+    stored = 2.0 ** -8 * dz.abs()
+    stored[rows, at] = 2.0 ** -16 * dz[rows, at].abs()
+    other = dl * (p * (2 * ez + 2.0 ** -18) + 2.0 ** -23)
+    for got, e, x, b, terms in ((dh, stored + other, dz, Wd, vocab),
+                                (dW, ((2.0 ** -16 if kept else 2.0 ** -8) * dz.abs() + other).T, dz.T, hd, tokens)):
+        ref = x @ b
+        bound = e @ b.abs() + (terms / 8 + 32) * U * (x.abs() @ b.abs()) + BF * ref.abs()
+        assert torch.all((got.double() - ref).abs() <= bound * (1 + 2.0 ** -6) + 1e-38)
