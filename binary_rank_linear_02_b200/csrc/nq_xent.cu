@@ -137,7 +137,9 @@ __device__ __forceinline__ float xent_ex2(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum { kStats = 0, kDz = 1, kToBf16 = 2, kPartial = 3 };
+// (kMadeUp: as bf16 too, dW with what bf16 left of dz at the labels added; apart, since dW of few tokens is
+// all epilogue and loses 4% to the registers for it)
+enum { kStats = 0, kDz = 1, kToBf16 = 2, kPartial = 3, kMadeUp = 4 };
 
 // "Token" and "class" in a transposed product (kT) change places: rows are classes (or
 // elements of d), columns are tokens.
@@ -147,10 +149,10 @@ struct XentEpilogue {
     int64_t label0;         // first class of the product
     union {
         int64_t vocab;      // all classes (kPartial: those up to the product's end)
-        int64_t tokens;     // kToBf16: how many labels there are
+        int64_t tokens;     // kMadeUp: how many labels there are
     };
     // rest, not kStats: what bf16 leaves of dz at each token's label, fp32 (null: it is not kept apart).
-    // kDz writes it; kPartial (dh) adds it times the label's row of W, kToBf16 (dW) times the token's row
+    // kDz writes it; kPartial (dh) adds it times the label's row of W, kMadeUp (dW) times the token's row
     // of h, to the class's row.
     union {
         float2* stats;      // kStats: [token][slot]: maximum, sum of exp(z - maximum)
@@ -166,7 +168,7 @@ struct XentEpilogue {
     };
     const float* lse;       // kDz, per token
     const float* dloss;     // kDz, per token
-    uint16_t* out;          // kDz, kToBf16: bf16, [row][column] with pitch ldo (kT: [column][row])
+    uint16_t* out;          // kDz, kToBf16, kMadeUp: bf16, [row][column] with pitch ldo (kT: [column][row])
     int64_t ldo;
     int low;                // kDz: what bf16 leaves of dz goes this many rows (kT: columns) on (0: nowhere)
     float* part;            // kPartial: [split][row][column] fp32 (kT: [split][column][row]), added to unless first
@@ -496,18 +498,21 @@ __device__ __forceinline__ void xent_columns_t(const XentEpilogue& e, float (&v)
         const float sum = across_lanes(v, lane, [](float a, float b) { return a + b; });
         if (lane < n) e.stats[(col + lane) * e.slots + slot] = make_float2(top, sum);
     } else {
-        [[maybe_unused]] uint16_t w[32];  // (what bf16 left of dz at the tokens' labels is to be multiplied by)
         if constexpr (kEpi == kPartial) {
+            if (e.rest) {  // what bf16 left of dz at the tokens' labels
+                uint16_t w[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int label = __shfl_sync(0xffffffffu, tok.label, j);
-                w[j] = label >= 0 && there ? e.other[(int64_t)label * e.rows + row] : 0;
+                for (int j = 0; j < 32; ++j) {
+                    const int label = __shfl_sync(0xffffffffu, tok.label, j);
+                    w[j] = label >= 0 && there ? e.other[(int64_t)label * e.rows + row] : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = fmaf(__shfl_sync(0xffffffffu, tok.dl, j), xent_float(w[j]), v[j]);
             }
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             float x = v[j];
-            if constexpr (kEpi == kPartial) x = fmaf(__shfl_sync(0xffffffffu, tok.dl, j), xent_float(w[j]), x);
             if constexpr (kEpi == kDz) {
                 const float p = xent_ex2(fmaf(x, kLog2e, -__shfl_sync(0xffffffffu, tok.lse2, j)));
                 const float dl = __shfl_sync(0xffffffffu, tok.dl, j);
@@ -570,7 +575,7 @@ __device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr,
             });
         }
     } else {
-        if constexpr (kEpi == kToBf16) {
+        if constexpr (kEpi == kMadeUp) {
             if (matches.most > kXOwn) {  // (the staging serves the sums first, then half as wide rows of results)
 #pragma unroll 1
                 for (int c0 = 0; c0 < left; c0 += 32) {
@@ -621,7 +626,7 @@ __device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr,
                         for (int j = 0; j < 32; ++j) v[j] = xent_rest(v[j]);
                     }
                 }
-                if constexpr (kEpi == kToBf16) {
+                if constexpr (kEpi == kMadeUp) {
 #pragma unroll
                     for (int k = 0; k < kXOwn; ++k) {
                         if (k >= matches.most) break;
@@ -638,7 +643,7 @@ __device__ __forceinline__ void xent_rows(const XentEpilogue& e, uint32_t taddr,
             }
             staging_write(buffer, lane, [&](int r, int p, uint4 w) {
                 // (dz: whole tiles, its rows are as long; dW, dh: cols is a multiple of 8)
-                if (row0 + r >= e.rows || (kEpi == kToBf16 && c0 + 8 * p >= left)) return;
+                if (row0 + r >= e.rows || (kEpi != kDz && c0 + 8 * p >= left)) return;
                 *reinterpret_cast<uint4*>(e.out + (row0 + r + (c >= 128 ? e.low : 0)) * e.ldo + col0 + c0 + 8 * p) = w;
             });
         }
@@ -836,9 +841,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
         int n = 0;
         bool ok = true;
         [[maybe_unused]] int first_labels[8];  // (looked through for every tile)
-        if constexpr (kEpi == kToBf16 && !kT) {
-            if (e.rest) xent_load_labels(e.labels, (int)e.tokens, 0, lane, first_labels);
-        }
+        if constexpr (kEpi == kMadeUp) xent_load_labels(e.labels, (int)e.tokens, 0, lane, first_labels);
         for (int item = pair; item < items && ok; item += pairs) {
             int tm, tn, kb0, kb1;
             const int split = tile_of(item, tm, tn, kb0, kb1);
@@ -847,9 +850,7 @@ xent_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
             XentToken tok = xent_token<kEpi>(e, row0 + lane, !kT && row0 + lane < e.rows);
             XentMatches matches;
             matches.most = 0;
-            if constexpr (kEpi == kToBf16 && !kT) {  // (while the sums are under way)
-                if (e.rest) matches = xent_matches(xent_labels(e, row0), first_labels, col0, lane);
-            }
+            if constexpr (kEpi == kMadeUp) matches = xent_matches(xent_labels(e, row0), first_labels, col0, lane);  // (while the sums are under way)
             [[maybe_unused]] float z[128];  // (the sum of a tile's parts, where it may have several)
             if constexpr (kKeeps) {
 #pragma unroll
@@ -1225,7 +1226,8 @@ int xent_backward(const uint16_t* h, const uint16_t* W, const int32_t* labels, c
                 g.other = h;
                 g.tokens = tokens;
             }
-            rc = xent_launch<kToBf16, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream, e.low);
+            rc = g.rest ? xent_launch<kMadeUp, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream, e.low)
+                        : xent_launch<kToBf16, true, true, false>(dz, piece, h, d, nv, d, tokens, kXTile, 1, true, g, stream, e.low);
             if (rc != NQ_OK) return rc;
         }
         if (dh) {
