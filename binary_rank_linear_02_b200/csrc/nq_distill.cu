@@ -25,14 +25,16 @@
 // classes alone.  It also takes the classes of a row that lie outside its 16-byte boundaries, and
 // writes the listed classes' gradient, last, over the others'.
 //
-// What bounds it: HBM.  (Device times of a call by itself.)  777 x 50257 fp32 forward: 33 us (4.7 TB/s of logits).  1024 x 32000 fp32 to
-// bf16 gradients: 50 us, the logits and the gradient at 3.9 TB/s; 1024 rows are 2.3 rounds of the 444
-// CTAs.  4096 x 128000 bf16: 503 us, where rows of 256 KB no longer stay in L2 and HBM carries the
-// logits twice and the gradient once, at 6.2 TB/s.  Ways around the second reading lost: a cluster
+// What bounds it: HBM.  (Times in calls in a row.)  777 x 50257 fp32 forward: 33 us (4.7 TB/s of logits).
+// 1024 x 32000 fp32 to bf16 gradients: 54 us, the logits and the gradient at 3.6 TB/s; 1024 rows are 2.3
+// rounds of the 444 CTAs.  4096 x 128000 bf16: 517 to 548 us, where rows of 256 KB do not all stay in L2: HBM
+// carries the logits almost twice (1024 such rows: 1.66 times) and the gradient once.  Where rows are short the teacher's warp bounds it:
+// 4096 x 1000 fp32 forward, 64 listed: 40 us, some 4 us a row.  Ways around the second reading lost: a cluster
 // that keeps a row in its shared memory (its reductions, 20 us of a row's life, left HBM idle), and
-// one CTA of 16 warps per SM that keeps what its ring holds (484 us here, but 62 in place of 50 for
-// the smaller rows: the time between the passes is filled by nothing); nor did half a row to each CTA
-// of a cluster, which leaves L2 half as many rows to keep, gain anything (541 us).  A second warp
+// one CTA of 16 warps per SM that keeps what its ring holds (on the device, by itself, 484 us where this
+// took 503, but 62 in place of 50 for the smaller rows: the time between the passes is filled by nothing);
+// nor did half a row to each CTA of a cluster, which leaves L2 half as many rows to keep, gain anything
+// (541 us).  A second warp
 // for the teacher (lists by one, sums by the other) made a call by itself 4% faster and calls in a
 // row 1% slower.
 #include <cuda_bf16.h>

@@ -37,10 +37,13 @@
 // more than the shared memory holds, the columns are taken in panels and the rows' sums are
 // kept between them.
 //
-// Measured: 32001 x 4096 (groups of 64 with zero points), 1 token: 25 us, 2.9 TB/s; 28672 x 8192
-// (groups of 128), 8 tokens: 37 us, 3.3 TB/s, of which x takes 5 to be brought in and launch and
-// pipeline about as long to start; in between instructions bound it, some 180 per 2048
-// weights.  Small matrices take 5 us.
+// Measured: 32001 x 4096 (groups of 64 with zero points), 1 token: 24 us, 3.05 TB/s; 28672 x 8192
+// (groups of 128), 8 tokens: 37 us, 3.3 TB/s.  Of these a third does not grow with the matrix (x, launch, the
+// pipeline's start: twice the rows take 27 us more under a profiler where the first take 41); in between it is
+// 4.5 TB/s and some 145 instructions, waits' polling included, per 16 x 128 weights, 2.3 of 4 a clock: not HBM,
+// not issue, not shared memory (half of its wavefronts) but the latency of dependent instructions, which four
+// warps a scheduler do not cover.  Every 8 tokens read and expand the codes again: 16 tokens 61 us, 1024
+// 3.6 ms.  Small matrices take 5 us on the device.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
