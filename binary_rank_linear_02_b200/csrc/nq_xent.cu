@@ -324,8 +324,11 @@ __device__ __forceinline__ void xent_dz32(float (&v)[32], int at, const XentToke
     for (int j = 0; j < 32; ++j) v[j] *= tok.dl;
 }
 
-// What bf16 leaves of a number.
-__device__ __forceinline__ float xent_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
+// What bf16 leaves of a number (nothing of an infinity).
+__device__ __forceinline__ float xent_rest(float x) {
+    const float rest = x - __bfloat162float(__float2bfloat16_rn(x));
+    return fabsf(rest) < INFINITY ? rest : 0.f;
+}
 __device__ __forceinline__ float xent_float(uint16_t bits) { return __uint_as_float((uint32_t)bits << 16); }
 
 // What a warp needs to find the tokens whose labels are among its 32 classes (lane = class).
@@ -524,7 +527,7 @@ __device__ __forceinline__ void xent_columns_t(const XentEpilogue& e, float (&v)
                     const __nv_bfloat16 high = __float2bfloat16_rn(x);
                     e.out[(col + j) * e.ldo + row] = __bfloat16_as_ushort(high);
                     e.out[(e.low + col + j) * e.ldo + row] =
-                        __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(high)));
+                        __bfloat16_as_ushort(__float2bfloat16_rn(xent_rest(x)));
                 }
             }
             if (j < n && there && (kEpi != kDz || !e.low)) {

@@ -241,3 +241,26 @@ def test_cross_entropy_many_tokens_of_few_classes(nq, tokens, kept):
         ref = x @ b
         bound = e @ b.abs() + (terms / 8 + 32) * U * (x.abs() @ b.abs()) + BF * ref.abs()
         assert torch.all((got.double() - ref).abs() <= bound * (1 + 2.0 ** -6) + 1e-38)
+
+
+@pytest.mark.parametrize("tokens,vocab", [(20, 300), (128, 300), (200, 1000), (200, 100), (600, 2000), (600, 500)])
+def test_cross_entropy_of_an_infinite_weight(nq, tokens, vocab):
+    """A token whose weight is infinite: its dz is infinite, +inf or -inf at its label, and dW what that times
+    its h is, not NaN (a second part of dz has nothing of an infinity); the other tokens' dh are as without it."""
+    d = 72
+    g = torch.Generator(device="cuda").manual_seed(44)
+    h = torch.randn(tokens, d, device="cuda", generator=g).bfloat16()
+    W = (torch.randn(vocab, d, device="cuda", generator=g) * 0.1).bfloat16()
+    labels = torch.randint(0, vocab, (tokens,), device="cuda", generator=g, dtype=torch.int32)
+    labels[5] = 7
+    dloss = torch.rand(tokens, device="cuda", generator=g) + 0.1
+    _, lse = nq.linear_cross_entropy_fwd(h, W, labels)
+    plain, _ = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    dloss[5] = float("inf")
+    dh, dW = nq.linear_cross_entropy_bwd(h, W, labels, lse, dloss)
+    sign = torch.ones(vocab, device="cuda")
+    sign[7] = -1.0
+    assert torch.all(h[5] != 0)
+    assert torch.equal(dW.float(), sign[:, None] * h[5].float()[None, :] * float("inf"))
+    others = torch.arange(tokens, device="cuda") != 5
+    assert torch.equal(dh[others], plain[others])
