@@ -443,7 +443,8 @@ int nq_distill_topk_bwd(const void* logits, int logits_type, int64_t ld, const i
  *             not count: loss 0 and dz = 0 (its lse is written, and its h must be finite)
  *   loss, lse : tokens float32 (written);  bwd reads lse as fwd wrote it
  *   dloss   : tokens float32
- *   dh : tokens x d bfloat16, dW : vocab x d bfloat16 (written; either may be NULL)
+ *   dh : tokens x d bfloat16, dW : vocab x d bfloat16 (written; either may be NULL; dh holds other
+ *             numbers until the call's work is done)
  *   scratch : at least nq_linear_cross_entropy_scratch_bytes(tokens, vocab, d, backward) bytes
  *             (scratch_bytes smaller: NQ_ERR_NOMEM), free again when the call's work is done
  *   tokens : 0 .. 1<<24 (else NQ_ERR_BATCH; with 0, bwd writes dW with zeros);  vocab : 1 ..
